@@ -466,6 +466,44 @@ MX_API int grouped_gemm_mxfp8_wgrad_ex(const uint8_t* dYc, const uint8_t* SFdYc,
                                        int64_t K, int64_t ld_tok, float* dW, int flags, int* dev_err,
                                        mx_stream_t stream);
 
+/*
+ * grouped_gemm_bf16_fwd / _dgrad / _wgrad -- the expert grouped products on bf16 operands, for
+ * layers kept in bf16 next to MXFP8 ones and for serving from bf16 weights.  off is the array
+ * of the MXFP8 calls: device int32 [E+1] from moe_permute, the experts' rows dense, any number
+ * of rows per expert (none too).  fp32 accumulation; no padding, no scale arrays, no workspace.
+ *
+ *   fwd    C[r][n]     = bf16( sum_k A[r][k] * W[e][n][k] )     off[e] <= r < off[e+1]
+ *          A bf16 [R x K], W bf16 [E x N x K], C bf16 [R x N]; rows >= off[E] are not written.
+ *   dgrad  dX[r][n]    = bf16( sum_k dY[r][k] * W[e][k][n] )
+ *          dY bf16 [R x K], W bf16 [E x K x N] (the weights as the forward call reads them: its
+ *          N is this call's K), dX bf16 [R x N]; rows >= off[E] are not written.
+ *   wgrad  dW[e][n][k] = sum over r in [off[e], off[e+1]) of dY[r][n] * X[r][k]
+ *          dY bf16 [R x N], X bf16 [R x K], dW fp32 [E x N x K]; 0 for an expert without rows.
+ *
+ * An expert's outputs depend on its own rows and weights only: NaN or Inf in another expert's,
+ * or in rows >= off[E], stay there.  Shapes: N % 8 == 0, K % 8 == 0, 1 <= E <= 1024; pointers
+ * 16-byte aligned.  R == 0 is allowed (nothing is written, or all of dW as 0).  Offsets that are
+ * not monotone from 0 or pass R set MX_DEVERR_BAD_SEGMENTS and nothing is written.
+ * dev_err required (MX_DEVERR_TIMEOUT, MX_DEVERR_BAD_SEGMENTS).
+ */
+MX_API int grouped_gemm_bf16_fwd(const void* A, const void* W, const int32_t* off, int E, int64_t R, int64_t N,
+                                 int64_t K, void* C, int* dev_err, mx_stream_t stream);
+MX_API int grouped_gemm_bf16_dgrad(const void* dY, const void* W, const int32_t* off, int E, int64_t R, int64_t N,
+                                   int64_t K, void* dX, int* dev_err, mx_stream_t stream);
+MX_API int grouped_gemm_bf16_wgrad(const void* dY, const void* X, const int32_t* off, int E, int64_t R, int64_t N,
+                                   int64_t K, float* dW, int* dev_err, mx_stream_t stream);
+
+/*
+ * moe_swiglu_fwd / moe_swiglu_bwd -- SwiGLU on bf16 rows without quantization, the activation
+ * between the bf16 products:
+ *   h  [R x I]  = bf16( silu(gate) * up ),  a = [gate | up] bf16 [R x 2I];
+ *   da [R x 2I] = [ bf16( dh * up * s * (1 + gate * (1 - s)) ) | bf16( dh * silu(gate) ) ],  s = sigmoid(gate),
+ * for dh bf16 [R x I]; fp32 arithmetic, one rounding.  da may be a (in place).  I % 8 == 0;
+ * pointers 16-byte aligned.
+ */
+MX_API int moe_swiglu_fwd(const void* a, int64_t R, int64_t I, void* h, mx_stream_t stream);
+MX_API int moe_swiglu_bwd(const void* dh, const void* a, int64_t R, int64_t I, void* da, mx_stream_t stream);
+
 /* Human-readable name of an mx_status value (static string). */
 MX_API const char* mx_status_str(int status);
 

@@ -89,6 +89,11 @@ def load(build_if_missing: bool = False):
                                                    P, P]),
         "grouped_gemm_mxfp8_dgrad_ex": (i32, [P, P, P, P, P, P, i32, i64, i64, i64, P, i32, P, P]),
         "grouped_gemm_mxfp8_wgrad_ex": (i32, [P, P, P, P, P, P, i32, i64, i64, i64, P, i32, P, P]),
+        "grouped_gemm_bf16_fwd": (i32, [P, P, P, i32, i64, i64, i64, P, P, P]),
+        "grouped_gemm_bf16_dgrad": (i32, [P, P, P, i32, i64, i64, i64, P, P, P]),
+        "grouped_gemm_bf16_wgrad": (i32, [P, P, P, i32, i64, i64, i64, P, P, P]),
+        "moe_swiglu_fwd": (i32, [P, i64, i64, P, P]),
+        "moe_swiglu_bwd": (i32, [P, P, i64, i64, P, P]),
         "mx_testing_grouped_gemm": (i32, [i32, P, P, P, P, P, P, i32, i64, i64, i64, i64, P, i32,
                                           ctypes.POINTER(TestingGemmOptions), P, P]),
         "mx_status_str": (ctypes.c_char_p, [i32]),
@@ -108,7 +113,8 @@ def exported_symbols():
             "grouped_gemm_mxfp8_fwd_swiglu", "grouped_gemm_mxfp8_dgrad", "grouped_gemm_mxfp8_wgrad",
             "grouped_gemm_mxfp8_fwd_ex", "grouped_gemm_mxfp8_fwd_swiglu_ex", "grouped_gemm_mxfp8_dgrad_ex",
             "grouped_gemm_mxfp8_wgrad_ex", "mx_testing_grouped_gemm", "moe_combine_bwd_ex", "mxfp8_gather_quantize_ex",
-            "mx_status_str"]
+            "grouped_gemm_bf16_fwd", "grouped_gemm_bf16_dgrad", "grouped_gemm_bf16_wgrad", "moe_swiglu_fwd",
+            "moe_swiglu_bwd", "mx_status_str"]
 
 
 def _ptr(t):
@@ -284,6 +290,33 @@ def grouped_gemm_mxfp8_wgrad_ex(dYc, SFdYc, Xc, SFXc, off, poff, E, N, K, ld_tok
     st = load().grouped_gemm_mxfp8_wgrad_ex(_ptr(dYc), _ptr(SFdYc), _ptr(Xc), _ptr(SFXc), _ptr(off), _ptr(poff), E,
                                             N, K, ld_tok, _ptr(dW), flags, _ptr(dev_err), _stream(stream))
     _check(st, "grouped_gemm_mxfp8_wgrad_ex")
+
+
+def grouped_gemm_bf16_fwd(A, W, off, E, R, N, K, C, dev_err, stream=None):
+    st = load().grouped_gemm_bf16_fwd(_ptr(A), _ptr(W), _ptr(off), E, R, N, K, _ptr(C), _ptr(dev_err), _stream(stream))
+    _check(st, "grouped_gemm_bf16_fwd")
+
+
+def grouped_gemm_bf16_dgrad(dY, W, off, E, R, N, K, dX, dev_err, stream=None):
+    st = load().grouped_gemm_bf16_dgrad(_ptr(dY), _ptr(W), _ptr(off), E, R, N, K, _ptr(dX), _ptr(dev_err),
+                                        _stream(stream))
+    _check(st, "grouped_gemm_bf16_dgrad")
+
+
+def grouped_gemm_bf16_wgrad(dY, X, off, E, R, N, K, dW, dev_err, stream=None):
+    st = load().grouped_gemm_bf16_wgrad(_ptr(dY), _ptr(X), _ptr(off), E, R, N, K, _ptr(dW), _ptr(dev_err),
+                                        _stream(stream))
+    _check(st, "grouped_gemm_bf16_wgrad")
+
+
+def moe_swiglu_fwd(a, R, I, h, stream=None):
+    st = load().moe_swiglu_fwd(_ptr(a), R, I, _ptr(h), _stream(stream))
+    _check(st, "moe_swiglu_fwd")
+
+
+def moe_swiglu_bwd(dh, a, R, I, da, stream=None):
+    st = load().moe_swiglu_bwd(_ptr(dh), _ptr(a), R, I, _ptr(da), _stream(stream))
+    _check(st, "moe_swiglu_bwd")
 
 
 def testing_grouped_gemm(pass_, A, SFA, B, SFB, off, poff, E, R, N, K, ld_tok, out, dev_err, flags=0,

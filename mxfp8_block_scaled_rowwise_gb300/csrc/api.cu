@@ -432,6 +432,65 @@ int grouped_gemm_mxfp8_wgrad_ex(const uint8_t* dYc, const uint8_t* SFdYc, const 
     return gemm_wgrad_common(dYc, SFdYc, Xc, SFXc, off, poff, E, N, K, ld_tok, dW, dev_err, stream, c);
 }
 
+namespace {
+int gemm_bf16_common(int pass, const void* A, const void* B, const int32_t* off, int E, int64_t R, int64_t N, int64_t K,
+                     void* out, int* dev_err, mx_stream_t stream) {
+    const bool wgrad = pass == mx::kBf16Wgrad;
+    if (E < 1 || E > 1024 || R < 0 || N <= 0 || K <= 0) return MX_ERR_INVALID_ARG;
+    if (!off || !dev_err) return MX_ERR_INVALID_ARG;
+    // without rows nothing of A (and of the weight gradient's B) is read, and only the weight gradient is written
+    if ((R > 0 && (!A || !B || !out)) || (wgrad && !out)) return MX_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 8 != 0) return MX_ERR_UNSUPPORTED;
+    if (R >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return MX_ERR_UNSUPPORTED;
+    if (ceil_div(N, 128) * ceil_div(K, 128) >= (int64_t(1) << 21)) return MX_ERR_UNSUPPORTED;
+    if (ceil_div(N, 128) * (ceil_div(R, 16) + E) >= (int64_t(1) << 31)) return MX_ERR_UNSUPPORTED;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(out)) return MX_ERR_ALIGNMENT;
+    int st = check_device();
+    if (st != MX_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (R == 0) {
+        if (!wgrad) return MX_OK;
+        return cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * K * sizeof(float), s) == cudaSuccess ? MX_OK
+                                                                                                         : MX_ERR_CUDA;
+    }
+    return mx::launch_grouped_gemm_bf16(pass, A, B, off, E, R, N, K, out, dev_err, s);
+}
+
+int swiglu_bf16_common(bool bwd, const void* dh, const void* a, int64_t R, int64_t I, void* out, mx_stream_t stream) {
+    if (R < 0 || I <= 0) return MX_ERR_INVALID_ARG;
+    if (I % 8 != 0) return MX_ERR_UNSUPPORTED;
+    if (R >= (int64_t(1) << 31) || I >= (int64_t(1) << 30) || R * (I / 8) >= (int64_t(1) << 38)) return MX_ERR_UNSUPPORTED;
+    if (R > 0 && (!a || !out || (bwd && !dh))) return MX_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(out) || (bwd && !aligned16(dh))) return MX_ERR_ALIGNMENT;
+    int st = check_device();
+    if (st != MX_OK) return st;
+    return mx::launch_swiglu_bf16(bwd, a, dh, R, I, out, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+int grouped_gemm_bf16_fwd(const void* A, const void* W, const int32_t* off, int E, int64_t R, int64_t N, int64_t K,
+                          void* C, int* dev_err, mx_stream_t stream) {
+    return gemm_bf16_common(mx::kBf16Fwd, A, W, off, E, R, N, K, C, dev_err, stream);
+}
+
+int grouped_gemm_bf16_dgrad(const void* dY, const void* W, const int32_t* off, int E, int64_t R, int64_t N, int64_t K,
+                            void* dX, int* dev_err, mx_stream_t stream) {
+    return gemm_bf16_common(mx::kBf16Dgrad, dY, W, off, E, R, N, K, dX, dev_err, stream);
+}
+
+int grouped_gemm_bf16_wgrad(const void* dY, const void* X, const int32_t* off, int E, int64_t R, int64_t N, int64_t K,
+                            float* dW, int* dev_err, mx_stream_t stream) {
+    return gemm_bf16_common(mx::kBf16Wgrad, dY, X, off, E, R, N, K, dW, dev_err, stream);
+}
+
+int moe_swiglu_fwd(const void* a, int64_t R, int64_t I, void* h, mx_stream_t stream) {
+    return swiglu_bf16_common(false, nullptr, a, R, I, h, stream);
+}
+
+int moe_swiglu_bwd(const void* dh, const void* a, int64_t R, int64_t I, void* da, mx_stream_t stream) {
+    return swiglu_bf16_common(true, dh, a, R, I, da, stream);
+}
+
 int mx_testing_grouped_gemm(int pass, const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB,
                             const int32_t* off, const int32_t* poff, int E, int64_t R, int64_t N, int64_t K,
                             int64_t ld_tok, void* out, int flags, const mx_testing_gemm_options* opt, int* dev_err,

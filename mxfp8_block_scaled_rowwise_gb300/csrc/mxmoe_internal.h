@@ -84,4 +84,13 @@ struct GemmProblem {
 
 int launch_grouped_gemm(const GemmProblem& pr, cudaStream_t stream);
 
+// bf16 grouped products; pass: kBf16Fwd (A [R x K], B [E x N x K], out bf16 [R x N]), kBf16Dgrad
+// (A [R x K], B [E x K x N], out bf16 [R x N]), kBf16Wgrad (A [R x N], B [R x K], out fp32 [E x N x K])
+enum GemmBf16Pass { kBf16Fwd = 0, kBf16Dgrad = 1, kBf16Wgrad = 2 };
+int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32_t* off, int E, int64_t R, int64_t N,
+                             int64_t K, void* out, int* dev_err, cudaStream_t stream);
+
+// SwiGLU on bf16 rows: out = h [R x I] from a [R x 2I], or (bwd) out = da [R x 2I] from dh and a
+int launch_swiglu_bf16(bool bwd, const void* a, const void* dh, int64_t R, int64_t I, void* out, cudaStream_t stream);
+
 }  // namespace mx

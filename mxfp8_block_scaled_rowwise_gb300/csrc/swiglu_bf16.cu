@@ -1,0 +1,70 @@
+// swiglu_bf16.cu -- SwiGLU and its backward on bf16 rows, without quantization: the activation
+// between the bf16 expert products.
+//
+//   forward   h  = bf16( g s u ),                       s = 1 / (1 + e^-g)
+//   backward  da = [ bf16( dh u s (1 + g (1 - s)) ) | bf16( dh g s ) ]
+//
+// for a = [g | u] bf16 [R x 2I].  fp32 arithmetic, one rounding at the end.  Bound by HBM: 6
+// bytes per h element forward (4 read, 2 written), 10 backward (6 read, 4 written).  One
+// thread takes 8 columns of a row: 16-byte loads and stores, every byte moved once.
+#include <cuda_runtime.h>
+
+#include "quant_common.cuh"
+#include "mxmoe_internal.h"
+
+namespace mx {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads) swiglu_bf16_kernel(const uint4* a, const uint4* dh, int64_t n,
+                                                               uint32_t Ic, uint4* out) {
+    // (out may be a: a thread reads its own gate and up columns before it writes them)
+    // chunk i covers columns 8 c .. 8 c + 7 of row r, i = r Ic + c, Ic = I / 8
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= n) return;
+    const int64_t r = i / Ic;
+    const int64_t c = i - r * Ic;
+    const int64_t at = r * 2 * Ic + c;
+    const uint4 gv = ld_stream_16(a + at), uv = ld_stream_16(a + at + Ic);
+    uint4 dv = make_uint4(0u, 0u, 0u, 0u);
+    if (BWD) dv = ld_stream_16(dh + i);
+    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
+    uint32_t o0[4], o1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float g0 = bf16_lo(gw[k]), g1 = bf16_hi(gw[k]), u0 = bf16_lo(uw[k]), u1 = bf16_hi(uw[k]);
+        const float s0 = sigmoid_f32(g0), s1 = sigmoid_f32(g1);
+        if (!BWD) {
+            o0[k] = pack_bf16x2(g0 * s0 * u0, g1 * s1 * u1);
+        } else {
+            const float d0 = bf16_lo(dw[k]), d1 = bf16_hi(dw[k]);
+            o0[k] = pack_bf16x2(d0 * u0 * (s0 * fmaf(g0, 1.0f - s0, 1.0f)), d1 * u1 * (s1 * fmaf(g1, 1.0f - s1, 1.0f)));
+            o1[k] = pack_bf16x2(d0 * (g0 * s0), d1 * (g1 * s1));
+        }
+    }
+    if (!BWD) {
+        out[i] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    } else {
+        out[at] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        out[at + Ic] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    }
+}
+
+}  // namespace
+
+int launch_swiglu_bf16(bool bwd, const void* a, const void* dh, int64_t R, int64_t I, void* out, cudaStream_t stream) {
+    const int64_t n = R * (I / 8);
+    const int64_t blocks = ceil_div(n, kThreads);
+    if (blocks == 0) return MX_OK;
+    const auto* a4 = static_cast<const uint4*>(a);
+    const auto* d4 = static_cast<const uint4*>(dh);
+    auto* o4 = static_cast<uint4*>(out);
+    const uint32_t Ic = static_cast<uint32_t>(I / 8);
+    if (bwd) swiglu_bf16_kernel<true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a4, d4, n, Ic, o4);
+    else swiglu_bf16_kernel<false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a4, d4, n, Ic, o4);
+    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
+}  // namespace mx
