@@ -504,6 +504,82 @@ MX_API int grouped_gemm_bf16_wgrad(const void* dY, const void* X, const int32_t*
 MX_API int moe_swiglu_fwd(const void* a, int64_t R, int64_t I, void* h, mx_stream_t stream);
 MX_API int moe_swiglu_bwd(const void* dh, const void* a, int64_t R, int64_t I, void* da, mx_stream_t stream);
 
+/*
+ * AdamW over many tensors at once, with the first and second moments in fp32 or in 8 bits, and
+ * the norm of all gradients that clips it.  For step t (counted from 1), per element:
+ *   g' = s g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, one launch for all tensors.
+ *
+ * adamw_tensor describes one tensor of n >= 1 elements (device pointers, contiguous):
+ *   param      bf16 or fp32 (param_dtype, MX_DTYPE_*), updated in place
+ *   grad       bf16 or fp32 (grad_dtype): e.g. the fp32 dW of the weight-gradient calls
+ *   moment, second   state_bits 32: m and v, fp32.  state_bits 8: one code byte per element,
+ *              m as E4M3 and r = sqrt(v) as 4 exponent and 4 mantissa bits without a sign
+ *              (code c > 0: (1 + (c & 15) / 16) 2^((c >> 4) - 15); 0: zero)
+ *   scale_m, scale_r   state_bits 8: one scale byte b (2^(b - 127)) per 32 elements,
+ *              ceil(n / 32) bytes each, any alignment; NULL for 32 bits.  b = 0 is a block of
+ *              zeros, 0xFF a block that held NaN or Inf and stays NaN
+ *   copy       bf16 copy of an fp32 param (e.g. the products' operand), written with it; or NULL
+ *   weight_decay, lr_mult   wd of the formula, and a factor on lr
+ * All-zero moments (and scales) are the initial state.  param, grad, moment, second and copy are
+ * 16-byte aligned; no two tensors overlap.
+ *
+ * adamw_plan checks the descriptors (HOST array) and fills *info (HOST); with image NULL that is
+ * all, else it also writes the plan's image into HOST memory of image_bytes >= info->bytes, which
+ * the caller copies to the device (16-byte aligned) and keeps with info while it trains.  The
+ * calls below take that device copy; they use words in it as scratch, so calls on one plan are
+ * ordered by the caller (one stream, or events).  The pointers in it must stay valid.
+ *
+ * adamw_grad_norm: out[0] = norm of all gradients of the plan, out[1] = the factor that brings it
+ * to max_norm: min(1, max_norm / norm); 1 for max_norm = 0; NaN where the norm is not finite
+ * (an element is NaN or Inf, or a square passes fp32's range).  Fixed summation order.
+ *
+ * adamw_step: step (device int64) counts the steps taken; the call reads t = *step + 1 and stores
+ * it.  lr_dev: device fp32 that replaces lr, or NULL.  grad_scale: device fp32 s (out + 1 of the
+ * norm), or NULL for 1; while it is NaN or Inf the call changes nothing, the step count included.
+ * 8-bit moments are rounded stochastically by a hash of (seed, t, position of the element in the
+ * plan: tensors one after another, each starting at a multiple of 32), so that changes far below
+ * one code add up; MX_ADAMW_STOCHASTIC does the same for bf16 params (else round to nearest).
+ * The same inputs give the same bytes.  0 <= beta < 1, 1e-30 <= eps, 0 <= lr.
+ *
+ * adamw_state_values: the values that 8-bit moments stand for, exactly, as bf16 at the elements'
+ * positions: moment, root (r = sqrt(v)) of info->positions elements each, 16-byte aligned; the
+ * gaps between tensors are not written.
+ */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* moment;
+    void* second;
+    uint8_t* scale_m;
+    uint8_t* scale_r;
+    void* copy;
+    int64_t n;
+    float weight_decay;
+    float lr_mult;
+    int32_t param_dtype;
+    int32_t grad_dtype;
+} adamw_tensor;
+
+typedef struct {
+    int64_t bytes;       /* size of the image */
+    int64_t positions;   /* sum over the tensors of n rounded up to 32 */
+    int64_t chunks;
+    int32_t tensors;
+    int32_t state_bits;
+} adamw_info;
+
+enum { MX_ADAMW_STOCHASTIC = 1 };
+
+MX_API int adamw_plan(const adamw_tensor* tensors, int n, int state_bits, void* image, size_t image_bytes,
+                      adamw_info* info);
+MX_API int adamw_grad_norm(void* plan, const adamw_info* info, double max_norm, float* out, mx_stream_t stream);
+MX_API int adamw_step(void* plan, const adamw_info* info, int64_t* step, double lr, double beta1, double beta2,
+                      double eps, const float* lr_dev, const float* grad_scale, uint32_t seed, int flags,
+                      mx_stream_t stream);
+MX_API int adamw_state_values(void* plan, const adamw_info* info, void* moment, void* root, mx_stream_t stream);
+
 /* Human-readable name of an mx_status value (static string). */
 MX_API const char* mx_status_str(int status);
 

@@ -33,6 +33,7 @@ MX_DEVERR_TIMEOUT = 2
 MX_DEVERR_BAD_SEGMENTS = 4
 MX_GEMM_B_SCALES_X1 = 1   # *_ex GEMM flag: B-operand scales in the plain one-copy layout
 MX_GEMM_B_BLOCKED = 2     # *_ex GEMM flag: B-operand codes in the blocked code layout
+MX_ADAMW_STOCHASTIC = 1   # adamw_step flag: bf16 parameters rounded stochastically
 MX_TESTING_FWD, MX_TESTING_DGRAD, MX_TESTING_WGRAD = 0, 1, 2
 
 
@@ -40,6 +41,21 @@ class TestingGemmOptions(ctypes.Structure):
     """mx_testing_gemm_options of include/mxmoe_testing.h (tests and A/B measurements only)."""
     _fields_ = [("ctas_per_mma", ctypes.c_int), ("wait_limit_ns", ctypes.c_uint64),
                 ("withhold_operands", ctypes.c_int), ("raster_group", ctypes.c_int), ("cluster_pairs", ctypes.c_int)]
+
+
+class AdamwTensor(ctypes.Structure):
+    """adamw_tensor of include/mxmoe.h."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("moment", ctypes.c_void_p),
+                ("second", ctypes.c_void_p), ("scale_m", ctypes.c_void_p), ("scale_r", ctypes.c_void_p),
+                ("copy", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("lr_mult", ctypes.c_float), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamwInfo(ctypes.Structure):
+    """adamw_info of include/mxmoe.h."""
+    _fields_ = [("bytes", ctypes.c_int64), ("positions", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("tensors", ctypes.c_int32), ("state_bits", ctypes.c_int32)]
+
 
 _lib = None
 
@@ -63,6 +79,7 @@ def load(build_if_missing: bool = False):
         _build.build()
     L = ctypes.CDLL(_build.LIB)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    f64 = ctypes.c_double
     sig = {
         "mx_sf_bytes": (sz, [i64, i64]),
         "mx_sf_bytes_x4": (sz, [i64, i64]),
@@ -94,6 +111,10 @@ def load(build_if_missing: bool = False):
         "grouped_gemm_bf16_wgrad": (i32, [P, P, P, i32, i64, i64, i64, P, P, P]),
         "moe_swiglu_fwd": (i32, [P, i64, i64, P, P]),
         "moe_swiglu_bwd": (i32, [P, P, i64, i64, P, P]),
+        "adamw_plan": (i32, [ctypes.POINTER(AdamwTensor), i32, i32, P, sz, ctypes.POINTER(AdamwInfo)]),
+        "adamw_grad_norm": (i32, [P, ctypes.POINTER(AdamwInfo), f64, P, P]),
+        "adamw_step": (i32, [P, ctypes.POINTER(AdamwInfo), P, f64, f64, f64, f64, P, P, ctypes.c_uint32, i32, P]),
+        "adamw_state_values": (i32, [P, ctypes.POINTER(AdamwInfo), P, P, P]),
         "mx_testing_grouped_gemm": (i32, [i32, P, P, P, P, P, P, i32, i64, i64, i64, i64, P, i32,
                                           ctypes.POINTER(TestingGemmOptions), P, P]),
         "mx_status_str": (ctypes.c_char_p, [i32]),
@@ -114,7 +135,7 @@ def exported_symbols():
             "grouped_gemm_mxfp8_fwd_ex", "grouped_gemm_mxfp8_fwd_swiglu_ex", "grouped_gemm_mxfp8_dgrad_ex",
             "grouped_gemm_mxfp8_wgrad_ex", "mx_testing_grouped_gemm", "moe_combine_bwd_ex", "mxfp8_gather_quantize_ex",
             "grouped_gemm_bf16_fwd", "grouped_gemm_bf16_dgrad", "grouped_gemm_bf16_wgrad", "moe_swiglu_fwd",
-            "moe_swiglu_bwd", "mx_status_str"]
+            "moe_swiglu_bwd", "adamw_plan", "adamw_grad_norm", "adamw_step", "adamw_state_values", "mx_status_str"]
 
 
 def _ptr(t):
@@ -317,6 +338,107 @@ def moe_swiglu_fwd(a, R, I, h, stream=None):
 def moe_swiglu_bwd(dh, a, R, I, da, stream=None):
     st = load().moe_swiglu_bwd(_ptr(dh), _ptr(a), R, I, _ptr(da), _stream(stream))
     _check(st, "moe_swiglu_bwd")
+
+
+class AdamwPlan:
+    """The tensors of an AdamW step as adamw_plan lays them out on the device, kept while training.
+
+    Holds the tensors it was made from: the plan has their addresses.  positions: elements of the
+    outputs of adamw_state_values; starts[i]: the position of tensor i's first element there."""
+
+    def __init__(self, device_image, info, tensors, starts):
+        self.image, self.info, self.tensors, self.starts = device_image, info, tensors, starts
+
+    @property
+    def positions(self) -> int:
+        return int(self.info.positions)
+
+    @property
+    def state_bits(self) -> int:
+        return int(self.info.state_bits)
+
+
+def _each(value, n):
+    if isinstance(value, (int, float)):
+        return [float(value)] * n
+    return [float(x) for x in value]
+
+
+def adamw_plan(params, grads, moments, seconds, scale_m=None, scale_r=None, copies=None, weight_decay=0.0, lr_mult=1.0,
+               stream=None) -> AdamwPlan:
+    """Plan of an AdamW step over lists of contiguous CUDA tensors (one entry per tensor).
+
+    moments / seconds: fp32 (m and v), or uint8 codes (m and sqrt(v)) with uint8 scale_m / scale_r of
+    ceil(n / 32) bytes each.  copies: bf16 copies of fp32 params (entries may be None).
+    weight_decay, lr_mult: a number, or one per tensor.  Copies the plan to the device on `stream`."""
+    n = len(params)
+    lists = dict(grads=grads, moments=moments, seconds=seconds, scale_m=scale_m, scale_r=scale_r, copies=copies)
+    lists = {k: list(v) if v is not None else [None] * n for k, v in lists.items()}
+    wd, mult = _each(weight_decay, n), _each(lr_mult, n)
+    if n == 0 or any(len(v) != n for v in lists.values()) or len(wd) != n or len(mult) != n:
+        raise MxError("adamw_plan: as many grads, moments, ... as params are wanted, one at least")
+    types = {torch.bfloat16: MX_DTYPE_BF16, torch.float32: MX_DTYPE_F32}
+    bits = 8 if lists["moments"][0].dtype == torch.uint8 else 32
+    state = torch.uint8 if bits == 8 else torch.float32
+    table, starts, pos = (AdamwTensor * n)(), [], 0
+    for i, p in enumerate(params):
+        row = {k: v[i] for k, v in lists.items()}
+        num = p.numel()
+        want = dict(grads=(num, tuple(types)), moments=(num, (state,)), seconds=(num, (state,)),
+                    copies=(num, (torch.bfloat16,)))
+        if bits == 8:
+            want.update(scale_m=((num + 31) // 32, (torch.uint8,)), scale_r=((num + 31) // 32, (torch.uint8,)))
+        if p.dtype not in types:
+            raise MxError("adamw_plan: tensor %d: params are bf16 or fp32, not %s" % (i, p.dtype))
+        for k, t in [("params", p)] + list(row.items()):
+            if t is None and (k == "copies" or (bits == 32 and k.startswith("scale"))):
+                continue
+            if t is None or (k != "params" and (k not in want or t.numel() != want[k][0] or t.dtype not in want[k][1])):
+                raise MxError("adamw_plan: tensor %d: %s is missing, or not of its size and type" % (i, k))
+            if not t.is_cuda or t.device != params[0].device or not t.is_contiguous():
+                raise MxError("adamw_plan: tensor %d: %s is not contiguous on the plan's device" % (i, k))
+        addr = {k: (t.data_ptr() if t is not None else None) for k, t in row.items()}
+        table[i] = AdamwTensor(p.data_ptr(), addr["grads"], addr["moments"], addr["seconds"], addr["scale_m"],
+                               addr["scale_r"], addr["copies"], num, wd[i], mult[i], types[p.dtype],
+                               types[row["grads"].dtype])
+        starts.append(pos)
+        pos += (num + 31) // 32 * 32
+    info = AdamwInfo()
+    _check(load().adamw_plan(table, n, bits, None, 0, ctypes.byref(info)), "adamw_plan")
+    image = torch.zeros(info.bytes, dtype=torch.uint8)
+    _check(load().adamw_plan(table, n, bits, ctypes.c_void_p(image.data_ptr()), info.bytes, ctypes.byref(info)),
+           "adamw_plan")
+    with torch.cuda.stream(torch.cuda.current_stream(params[0].device) if stream is None else stream):
+        dev_image = image.to(params[0].device)
+    return AdamwPlan(dev_image, info, (list(params), lists), starts)
+
+
+def adamw_grad_norm(plan: AdamwPlan, max_norm: float, out, stream=None):
+    """out (fp32 [2]) = norm of all gradients, and the factor that clips it to max_norm (0: no clipping)."""
+    if out.dtype != torch.float32 or out.numel() < 2:
+        raise MxError("adamw_grad_norm: out is fp32 [2]")
+    st = load().adamw_grad_norm(_ptr(plan.image), ctypes.byref(plan.info), max_norm, _ptr(out), _stream(stream))
+    _check(st, "adamw_grad_norm")
+
+
+def adamw_step(plan: AdamwPlan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, lr_dev=None, grad_scale=None, seed=0,
+               stochastic=False, stream=None):
+    """One AdamW step over the plan's tensors; step: int64 [1] on the device, the steps taken so far."""
+    if step.dtype != torch.int64 or any(t is not None and t.dtype != torch.float32 for t in (lr_dev, grad_scale)):
+        raise MxError("adamw_step: step is int64 [1], lr_dev and grad_scale are fp32 [1]")
+    st = load().adamw_step(_ptr(plan.image), ctypes.byref(plan.info), _ptr(step), lr, beta1, beta2, eps, _ptr(lr_dev),
+                           _ptr(grad_scale), seed & 0xFFFFFFFF, MX_ADAMW_STOCHASTIC if stochastic else 0,
+                           _stream(stream))
+    _check(st, "adamw_step")
+
+
+def adamw_state_values(plan: AdamwPlan, moment, root, stream=None):
+    """The values of 8-bit moments as bf16 [plan.positions] each: m, and r = sqrt(v)."""
+    if any(t.dtype != torch.bfloat16 or t.numel() < plan.positions for t in (moment, root)):
+        raise MxError("adamw_state_values: moment and root are bf16 [plan.positions]")
+    st = load().adamw_state_values(_ptr(plan.image), ctypes.byref(plan.info), _ptr(moment), _ptr(root),
+                                   _stream(stream))
+    _check(st, "adamw_state_values")
 
 
 def testing_grouped_gemm(pass_, A, SFA, B, SFB, off, poff, E, R, N, K, ld_tok, out, dev_err, flags=0,

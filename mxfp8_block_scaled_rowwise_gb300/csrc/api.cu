@@ -491,6 +491,48 @@ int moe_swiglu_bwd(const void* dh, const void* a, int64_t R, int64_t I, void* da
     return swiglu_bf16_common(true, dh, a, R, I, da, stream);
 }
 
+int adamw_plan(const adamw_tensor* tensors, int n, int state_bits, void* image, size_t image_bytes, adamw_info* info) {
+    if (!tensors || !info || n < 1 || n > (1 << 24) || (state_bits != 8 && state_bits != 32)) return MX_ERR_INVALID_ARG;
+    return mx::build_adamw_plan(tensors, n, state_bits, image, image_bytes, info);
+}
+
+namespace {
+int check_adamw(const void* plan, const adamw_info* info) {
+    if (!plan || !info || info->tensors < 1 || info->chunks < 1 || info->chunks >= (int64_t(1) << 31) ||
+        (info->state_bits != 8 && info->state_bits != 32))
+        return MX_ERR_INVALID_ARG;
+    return aligned16(plan) ? check_device() : MX_ERR_ALIGNMENT;
+}
+}  // namespace
+
+int adamw_grad_norm(void* plan, const adamw_info* info, double max_norm, float* out, mx_stream_t stream) {
+    if (!out || !(max_norm >= 0.0)) return MX_ERR_INVALID_ARG;
+    const int st = check_adamw(plan, info);
+    if (st != MX_OK) return st;
+    return mx::launch_adamw_norm(plan, *info, max_norm, out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int adamw_step(void* plan, const adamw_info* info, int64_t* step, double lr, double beta1, double beta2, double eps,
+               const float* lr_dev, const float* grad_scale, uint32_t seed, int flags, mx_stream_t stream) {
+    if (!step || (flags & ~MX_ADAMW_STOCHASTIC) != 0) return MX_ERR_INVALID_ARG;
+    if (!(lr >= 0.0 && lr < 1e30) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !(eps >= 1e-30 && eps < 1e30))
+        return MX_ERR_INVALID_ARG;
+    const int st = check_adamw(plan, info);
+    if (st != MX_OK) return st;
+    return mx::launch_adamw_step(plan, *info, step, lr, beta1, beta2, eps, lr_dev, grad_scale, seed,
+                                 (flags & MX_ADAMW_STOCHASTIC) != 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int adamw_state_values(void* plan, const adamw_info* info, void* moment, void* root, mx_stream_t stream) {
+    if (!moment || !root) return MX_ERR_INVALID_ARG;
+    const int st = check_adamw(plan, info);
+    if (st != MX_OK) return st;
+    if (info->state_bits != 8) return MX_ERR_INVALID_ARG;
+    if (!aligned16(moment) || !aligned16(root)) return MX_ERR_ALIGNMENT;
+    return mx::launch_adamw_values(plan, *info, moment, root, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int mx_testing_grouped_gemm(int pass, const uint8_t* A, const uint8_t* SFA, const uint8_t* B, const uint8_t* SFB,
                             const int32_t* off, const int32_t* poff, int E, int64_t R, int64_t N, int64_t K,
                             int64_t ld_tok, void* out, int flags, const mx_testing_gemm_options* opt, int* dev_err,

@@ -90,6 +90,14 @@ enum GemmBf16Pass { kBf16Fwd = 0, kBf16Dgrad = 1, kBf16Wgrad = 2 };
 int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32_t* off, int E, int64_t R, int64_t N,
                              int64_t K, void* out, int* dev_err, cudaStream_t stream);
 
+// AdamW (adamw.cu).  image == nullptr: checks the tensors and fills *info only.
+int build_adamw_plan(const adamw_tensor* tensors, int n, int state_bits, void* image, size_t image_bytes,
+                     adamw_info* info);
+int launch_adamw_step(void* plan, const adamw_info& info, int64_t* step, double lr, double beta1, double beta2, double eps,
+                      const float* lr_dev, const float* grad_scale, uint32_t seed, bool stochastic, cudaStream_t stream);
+int launch_adamw_norm(void* plan, const adamw_info& info, double max_norm, float* out, cudaStream_t stream);
+int launch_adamw_values(void* plan, const adamw_info& info, void* moment, void* root, cudaStream_t stream);
+
 // SwiGLU on bf16 rows: out = h [R x I] from a [R x 2I], or (bwd) out = da [R x 2I] from dh and a
 int launch_swiglu_bf16(bool bwd, const void* a, const void* dh, int64_t R, int64_t I, void* out, cudaStream_t stream);
 
