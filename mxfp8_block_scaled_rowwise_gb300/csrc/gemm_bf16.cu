@@ -1,103 +1,636 @@
-// gemm_bf16.cu -- expert grouped products on bf16 operands with ragged groups:
+// gemm_bf16.cu -- expert grouped products on bf16 operands with ragged groups, for sm_103a:
 //   forward  C[r]  = bf16( A[r] W_e^T )            rows r in [off[e], off[e + 1])
 //   dgrad    dX[r] = bf16( dY[r] W_e )
 //   wgrad    dW[e] = sum over the expert's rows of dY[r]^T X[r]   (fp32; zeros without rows)
-// fp32 accumulation.  One CTA per 64 x 64 output tile, operands through shared memory as fp32,
-// every index checked against the expert's own extent.
-#include <cuda_bf16.h>
+//
+// The three passes are one contraction D[m][n] = sum_k a(m, k) b(n, k) that differs in which
+// dimension of each operand is contiguous in memory:
+//            a(m, k)              b(n, k)                  k runs over
+//   forward  A[r0 + m][k]    k    W[e][n][k]          k    the row width
+//   dgrad    dY[r0 + m][k]   k    W[e][k][n]          n    the forward's output width
+//   wgrad    dY[r0 + k][m]   m    X[r0 + k][n]        n    the expert's rows
+// No operand is transposed in memory: tcgen05.mma takes either orientation from shared memory
+// (K contiguous, or M / N contiguous), in both cases as 128-byte rows with the 128-byte swizzle.
+//
+// Ragged edges.  An expert's rows are dense, so a tile of A rows can reach into the next expert's
+// rows: those only feed accumulator rows that are never stored.  Widths that no tile divides end
+// in zeros that the tensor copies fill in (the weights have a dimension of their own for the
+// expert, so a tile never reads the next expert's).  Only wgrad contracts over rows: the last 64
+// of an expert's rows would add the next expert's, and a NaN there times a zero would not vanish,
+// so one warp per CTA overwrites those rows of both operands with zeros in shared memory before
+// the MMA sees the stage.
+//
+// Roles of the 12 warps: 0 issues the tensor copies, 1 (one lane of the leader CTA) the MMAs, 2
+// builds the tile list and zeroes wgrad's ragged ends, 4 to 11 drain the accumulators.  With
+// NC = 2 a cluster of two CTAs computes 256 x 256 tiles with cta_group::2 MMAs, each CTA staging
+// its 128 rows of a and one half of b; with NC = 1 a CTA computes 128 x 256 tiles.  The 512
+// columns of tensor memory hold two accumulators, so a tile is drained while the next one is
+// multiplied.  A persistent grid walks the tile list; an expert's tiles are contiguous, M fastest.
+// Every wait is bounded; one that runs out sets MX_DEVERR_TIMEOUT and all roles leave.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include "ptx.cuh"
 #include "mxmoe_internal.h"
 
 namespace mx {
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kDepth = 16;
-constexpr int kThreads = 256;
-constexpr int kFwd = kBf16Fwd, kDgrad = kBf16Dgrad, kWgrad = kBf16Wgrad;
+constexpr int BM = 128;        // accumulator rows per CTA
+constexpr int BN = 256;        // tile columns
+constexpr int BK = 64;         // elements per K step: one 128-byte swizzled row
+constexpr uint32_t kRowBytes = 128;
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kNumEpiWarps = 8;
+constexpr int kMaxE = 1024;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s: far above any legitimate wait
+// wgrad: rows summed in tensor memory before the partial sum moves to registers.  The tensor
+// core's fp32 additions truncate, so a sum's relative error grows with its length (measured with
+// a library product of 4096 rows: 4.4e-6, and 4.7e-7 at 512); partial sums of 512 rows added in
+// registers, rounded to nearest, keep it where an fp32 sum has it.
+constexpr int kPartSteps = 8;
 
-__device__ bool offsets_ok(const int32_t* off, int E, int64_t R) {
-    bool bad = false;
-    for (int e = threadIdx.x; e < E; e += kThreads) bad |= off[e + 1] < off[e];
-    if (threadIdx.x == 0) bad |= off[0] != 0 || off[E] > R;
-    return !__syncthreads_or(bad);
+template <int NC>
+struct Cfg {
+    static constexpr int kSub = NC;                               // K steps per pipeline stage
+    static constexpr int kStages = NC == 1 ? 4 : 3;
+    static constexpr int kSlots = kStages * kSub;
+    static constexpr int kTileM = BM * NC;
+    static constexpr int kBRows = BN / NC;                        // b rows staged per CTA
+    static constexpr uint32_t kABytes = BM * kRowBytes;
+    static constexpr uint32_t kBBytes = kBRows * kRowBytes;
+    static constexpr uint32_t kOffA = 0;
+    static constexpr uint32_t kOffB = kSlots * kABytes;
+    static constexpr uint32_t kOffBar = kOffB + kSlots * kBBytes;
+    static constexpr uint32_t kNumBars = 3 * kStages + 5;         // full[], empty[], tail[], tmem_full[2], tmem_empty[2], drain
+    static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag
+    static constexpr uint32_t kOffTable = (kOffMisc + 8 + 15) / 16 * 16;
+    static constexpr uint32_t kSmemBytes = kOffTable + (kMaxE + 1) * 4 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct Args {
+    const int32_t* off;
+    int E;
+    int64_t R;             // rows of A (dY): off[E] may not pass it
+    int64_t m_out, n_out;  // wgrad: rows of dW[e]; all: columns of the output
+    int64_t k_len;         // forward, dgrad: contraction length
+    void* out;
+    int wide_store;        // output rows start on 32-byte boundaries: whole-sector stores
+    int* dev_err;
+};
+
+struct Tile {
+    int e;
+    int64_t row0;          // first row of the expert
+    int64_t m_in;          // this CTA's first tile row: within the expert's rows, or within m_out
+    int64_t n0;            // first output column of the tile
+    int num_kt;            // K steps
+    int tail;              // wgrad: rows of the last K step that are the expert's, 0 if all 64
+    int valid_rows;        // of this CTA's 128
+};
+
+template <int NC, bool WGRAD>
+__device__ __forceinline__ Tile get_tile(const Args& g, const int32_t* table, int64_t L, uint32_t rank) {
+    constexpr int TM = Cfg<NC>::kTileM;
+    Tile t;
+    const int64_t nt = (g.n_out + BN - 1) / BN;
+    int64_t local;
+    if (WGRAD) {
+        const int64_t per_e = ((g.m_out + TM - 1) / TM) * nt;
+        t.e = static_cast<int>(L / per_e);
+        local = L - t.e * per_e;
+    } else {
+        int lo = 0, hi = g.E - 1;   // last e with table[e] <= L
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (table[mid] <= L) lo = mid; else hi = mid - 1;
+        }
+        t.e = lo;
+        local = L - table[lo];
+    }
+    t.row0 = __ldg(g.off + t.e);
+    const int64_t te = static_cast<int64_t>(__ldg(g.off + t.e + 1)) - t.row0;
+    // Groups of G M tiles, M fastest inside a group: the CTAs in flight share one b tile, and the
+    // group's strip of a (at most 32 MiB) stays in L2 across the N tiles.
+    const int64_t rows = WGRAD ? g.m_out : te;
+    const int64_t kbytes = 2 * (WGRAD ? te : g.k_len);
+    const int64_t mts = (rows + TM - 1) / TM;
+    int64_t G = (int64_t(32) << 20) / (TM * (kbytes > 0 ? kbytes : 1));
+    G = G < 1 ? 1 : (G > mts ? mts : G);
+    const int64_t grp = local / (G * nt);
+    const int64_t in = local - grp * G * nt;
+    const int64_t gs = mts - grp * G < G ? mts - grp * G : G;
+    const int64_t ntile = in / gs;
+    t.m_in = (grp * G + (in - ntile * gs)) * TM + static_cast<int64_t>(rank) * BM;
+    t.n0 = ntile * BN;
+    const int64_t k = WGRAD ? te : g.k_len;
+    t.num_kt = static_cast<int>((k + BK - 1) / BK);
+    t.tail = WGRAD ? static_cast<int>(k % BK) : 0;
+    const int64_t vr = rows - t.m_in;
+    t.valid_rows = static_cast<int>(vr < 0 ? 0 : (vr < BM ? vr : BM));
+    return t;
 }
 
-template <int PASS>
-__global__ void __launch_bounds__(kThreads) grouped_bf16_kernel(const __nv_bfloat16* A, const __nv_bfloat16* B,
-                                                                const int32_t* off, int E, int64_t R, int64_t N,
-                                                                int64_t K, void* out, int* dev_err) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    if (!offsets_ok(off, E, R)) {
-        if (threadIdx.x == 0) atomicOr(dev_err, MX_DEVERR_BAD_SEGMENTS);
-        return;
-    }
-    int e = 0;
-    int64_t m0 = 0;   // first output row of the tile: within the expert's rows, or within N (wgrad)
-    if (PASS == kWgrad) {
-        const int64_t mt = (N + kTile - 1) / kTile;
-        e = static_cast<int>(blockIdx.y / mt);
-        m0 = (blockIdx.y - e * mt) * kTile;
+// Loads of one K step: this CTA's 128 rows of a and kBRows of b (from row b0 = its first b row).
+// G selects whether the copies complete on a barrier in the pair's leader (2) or in this CTA (1).
+template <int NC, int PASS, int G>
+__device__ __forceinline__ void load_step(const CUtensorMap* tmA, const CUtensorMap* tmB, uint32_t sa, uint32_t sb,
+                                          uint32_t bar, const Tile& t, int kt, int32_t b0) {
+    const int32_t k0 = kt * BK;
+    const int32_t row0 = static_cast<int32_t>(t.row0), m = static_cast<int32_t>(t.m_in);
+    if constexpr (PASS != kBf16Wgrad) {
+        tma_load_2d_g<G>(sa, tmA, bar, k0, row0 + m);
     } else {
-        int64_t left = blockIdx.y;
-        for (; e < E; ++e) {
-            const int64_t t = (static_cast<int64_t>(off[e + 1]) - off[e] + kTile - 1) / kTile;
-            if (left < t) break;
-            left -= t;
-        }
-        if (e == E) return;
-        m0 = left * kTile;
+#pragma unroll
+        for (int i = 0; i < BM / 64; ++i) tma_load_2d_g<G>(sa + i * 64 * kRowBytes, tmA, bar, m + 64 * i, row0 + k0);
     }
-    const int64_t r0 = off[e], rows = static_cast<int64_t>(off[e + 1]) - r0;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const int64_t M = PASS == kWgrad ? N : rows, cols = PASS == kWgrad ? K : N, depth = PASS == kWgrad ? rows : K;
-    float acc[4][4] = {};
-    const int tm = threadIdx.x / 16 * 4, tn = threadIdx.x % 16 * 4;
-    for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            const int x = PASS == kWgrad ? i % kTile : i / kDepth, k = PASS == kWgrad ? i / kTile : i % kDepth;
-            const bool in = m0 + x < M && k0 + k < depth;
-            sa[k][x] = in ? __bfloat162float(PASS == kWgrad ? A[(r0 + k0 + k) * N + m0 + x] : A[(r0 + m0 + x) * K + k0 + k]) : 0.f;
+    if constexpr (PASS == kBf16Fwd) {
+        tma_load_3d_g<G>(sb, tmB, bar, k0, b0, t.e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Cfg<NC>::kBRows / 64; ++i) {
+            if constexpr (PASS == kBf16Dgrad) tma_load_3d_g<G>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, k0, t.e);
+            else tma_load_2d_g<G>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, row0 + k0);
         }
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            const int x = PASS == kFwd ? i / kDepth : i % kTile, k = PASS == kFwd ? i % kDepth : i / kTile;
-            const bool in = n0 + x < cols && k0 + k < depth;
-            const int64_t at = PASS == kFwd ? (e * N + n0 + x) * K + k0 + k
-                               : PASS == kDgrad ? (e * K + k0 + k) * N + n0 + x : (r0 + k0 + k) * K + n0 + x;
-            sb[k][x] = in ? __bfloat162float(B[at]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][tm + i], sb[k][tn + j], acc[i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            if (m0 + tm + i >= M || n0 + tn + j >= cols) continue;
-            const int64_t at = ((PASS == kWgrad ? e * N : r0) + m0 + tm + i) * cols + n0 + tn + j;
-            if (PASS == kWgrad) static_cast<float*>(out)[at] = acc[i][j];
-            else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(acc[i][j]);
+}
+
+template <int NC, int PASS>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args g) {
+    using C = Cfg<NC>;
+    constexpr bool kW = PASS == kBf16Wgrad;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + C::kOffBar;                     // + 8 * stage (used in the leader)
+    const uint32_t bar_empty = bar_full + 8 * C::kStages;             // + 8 * stage
+    const uint32_t bar_tail = bar_full + 16 * C::kStages;             // + 8 * stage: this CTA's copies of a ragged last stage
+    const uint32_t bar_tmem_full = bar_full + 24 * C::kStages;        // + 8 * accumulator
+    const uint32_t bar_tmem_empty = bar_tmem_full + 16;               // + 8 * accumulator (used in the leader)
+    const uint32_t bar_drain = bar_tmem_full + 32;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    int32_t* table = reinterpret_cast<int32_t*>(smem + C::kOffTable);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = NC == 2 ? cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int64_t unit = blockIdx.x / NC;
+    const int64_t num_units = gridDim.x / NC;
+    const uint32_t lead_full = NC == 2 ? mapa_shared(bar_full, 0) : bar_full;
+    const uint32_t lead_tmem_empty = NC == 2 ? mapa_shared(bar_tmem_empty, 0) : bar_tmem_empty;
+    const uint16_t pair_ctas = static_cast<uint16_t>(NC == 2 ? 0x3 : 0x1);
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            // wgrad: one arrival per CTA (its producer, or for a ragged last stage its zeroing warp)
+            mbar_init(bar_full + 8 * s, kW ? NC : 1);
+            mbar_init(bar_empty + 8 * s, 1);
+            mbar_init(bar_tail + 8 * s, 1);
         }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar_tmem_full + 8 * a, 1);
+            mbar_init(bar_tmem_empty + 8 * a, kNumEpiWarps * NC);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_g<NC>(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish_g<NC>();
+    }
+    if (warp == 2) {
+        // Validate the offsets (every later address depends on them) and build the tile list:
+        // table[e] = first tile of expert e, table[E] = tile count.
+        const int64_t nt = (g.n_out + BN - 1) / BN;
+        const int per = (g.E + 31) / 32;
+        const int e0 = lane * per;
+        int32_t sum = 0;
+        bool bad = false;
+        for (int e = e0; e < e0 + per && e < g.E; ++e) {
+            const int64_t te = static_cast<int64_t>(__ldg(g.off + e + 1)) - __ldg(g.off + e);
+            bad |= te < 0;
+            if (!kW && te > 0) sum += static_cast<int32_t>((te + C::kTileM - 1) / C::kTileM * nt);
+        }
+        if (lane == 31) bad |= __ldg(g.off) != 0 || __ldg(g.off + g.E) > g.R;
+        bad = __any_sync(0xffffffffu, bad);
+        int32_t incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        if (!kW && !bad) {
+            int32_t run = incl - sum;
+            for (int e = e0; e < e0 + per && e < g.E; ++e) {
+                const int64_t te = static_cast<int64_t>(__ldg(g.off + e + 1)) - __ldg(g.off + e);
+                table[e] = run;
+                run += static_cast<int32_t>((te + C::kTileM - 1) / C::kTileM * nt);
+            }
+        }
+        if (lane == 31) {
+            table[g.E] = bad ? 0 : kW ? static_cast<int32_t>(g.E * ((g.m_out + C::kTileM - 1) / C::kTileM) * nt) : incl;
+            if (bad && leader) atomicOr(g.dev_err, MX_DEVERR_BAD_SEGMENTS);
+        }
+    }
+    tc_fence_before();
+    if (NC == 2) cluster_sync(); else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int64_t total_tiles = table[g.E];
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            uint32_t tails = 0;   // bit s: parity of the next tail phase of stage s; bit 8 + s: one was issued
+            bool ok = true;
+            for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
+                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                const int32_t b0 = static_cast<int32_t>(t.n0 + rank * C::kBRows);
+                for (int kt = 0; kt < t.num_kt; kt += C::kSub) {
+                    const int nsub = t.num_kt - kt < C::kSub ? t.num_kt - kt : C::kSub;
+                    if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bytes = static_cast<uint32_t>(nsub) * (C::kABytes + C::kBBytes);
+                    if (kW && t.tail != 0 && kt + nsub == t.num_kt) {
+                        // the ragged last stage: to this CTA's own barrier, for the zeroing warp
+                        mbar_arrive_expect_tx(bar_tail + 8 * stage, bytes);
+                        for (int sub = 0; sub < nsub; ++sub) {
+                            const int slot = stage * C::kSub + sub;
+                            load_step<NC, PASS, 1>(&tmA, &tmB, sbase + C::kOffA + slot * C::kABytes,
+                                                   sbase + C::kOffB + slot * C::kBBytes, bar_tail + 8 * stage, t, kt + sub, b0);
+                        }
+                        tails = (tails ^ (1u << stage)) | (0x100u << stage);
+                    } else {
+                        if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, NC * bytes);
+                        else if (kW) mbar_arrive_cluster_relaxed(lead_full + 8 * stage);
+                        for (int sub = 0; sub < nsub; ++sub) {
+                            const int slot = stage * C::kSub + sub;
+                            load_step<NC, PASS, NC>(&tmA, &tmB, sbase + C::kOffA + slot * C::kABytes,
+                                                    sbase + C::kOffB + slot * C::kBBytes, lead_full + 8 * stage, t,
+                                                    kt + sub, b0);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+            }
+            // let the copies still in flight land before exit
+            for (int s = 0; s < C::kStages; ++s)
+                if ((tails >> (8 + s)) & 1u) mbar_wait_timeout(bar_tail + 8 * s, ((tails >> s) & 1u) ^ 1u, kWaitLimitNs / 4);
+            if (leader) {
+                const int64_t outstanding = issued < C::kStages ? issued : C::kStages;
+                for (int64_t i = 1; i <= outstanding; ++i) {
+                    const int64_t idx = issued - i;
+                    mbar_wait_timeout(bar_full + 8 * static_cast<int>(idx % C::kStages),
+                                      static_cast<uint32_t>((idx / C::kStages) & 1), kWaitLimitNs / 4);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader CTA)
+        if (lane == 0 && leader) {
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t acc_iter = 0;   // accumulations begun: accumulator acc_iter & 1
+            bool ok = true;
+            constexpr uint32_t idesc = idesc_bf16(C::kTileM, BN, kW, PASS != kBf16Fwd);
+            // K contiguous: rows of 128 B, 8-row groups 1 KiB apart; 16 K = 32 bytes further.
+            // M / N contiguous: 64 of them per 128-byte row, the next 64 at 8 KiB; 8-K groups
+            // 1 KiB apart; 16 K = two groups further.
+            constexpr uint32_t kLboA = kW ? 64 * kRowBytes : 16, kLboB = PASS != kBf16Fwd ? 64 * kRowBytes : 16;
+            constexpr uint64_t kStepA = kW ? 2048 >> 4 : 32 >> 4, kStepB = PASS != kBf16Fwd ? 2048 >> 4 : 32 >> 4;
+            for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
+                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                for (int kt = 0; kt < t.num_kt && ok; kt += C::kSub) {
+                    const uint32_t acc = acc_iter & 1u;
+                    const bool first = kW ? kt % kPartSteps == 0 : kt == 0;
+                    if (first) {
+                        if (!mbar_wait_bounded(bar_tmem_empty + 8 * acc, ((acc_iter >> 1) & 1u) ^ 1u, abort_flag,
+                                               kWaitLimitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    const int nsub = t.num_kt - kt < C::kSub ? t.num_kt - kt : C::kSub;
+                    const bool there = kW && NC == 2
+                                           ? mbar_wait_bounded_cluster(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs)
+                                           : mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs);
+                    if (!there) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int sub = 0; sub < C::kSub; ++sub) {
+                        if (sub < nsub) {
+                            const int slot = stage * C::kSub + sub;
+                            const uint64_t adesc = smem_desc(sbase + C::kOffA + slot * C::kABytes, kLboA, 1024, 2);
+                            const uint64_t bdesc = smem_desc(sbase + C::kOffB + slot * C::kBBytes, kLboB, 1024, 2);
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k)
+                                mma_bf16_g<NC>(tmem_base + acc * BN, adesc + k * kStepA, bdesc + k * kStepB, idesc,
+                                               (first && sub == 0 && k == 0) ? 0u : 1u);
+                        }
+                    }
+                    tc_commit_g<NC>(bar_empty + 8 * stage, pair_ctas);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    const int next = kt + C::kSub;
+                    if (next >= t.num_kt || (kW && next % kPartSteps == 0)) {
+                        tc_commit_g<NC>(bar_tmem_full + 8 * acc, pair_ctas);
+                        ++acc_iter;
+                    }
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+            }
+            // every tcgen05 operation this thread issued has finished once this arrives
+            tc_commit_g<NC>(bar_drain, static_cast<uint16_t>(0x1));
+            mbar_wait_timeout(bar_drain, 0, kWaitLimitNs / 4);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ wgrad: ragged last stages
+        if (kW) {
+            int64_t stages = 0;
+            uint32_t tails = 0;   // bit s: parity of stage s's next tail phase
+            for (int64_t L = unit; L < total_tiles; L += num_units) {
+                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                stages += (t.num_kt + C::kSub - 1) / C::kSub;
+                if (t.tail == 0) continue;
+                const int stage = static_cast<int>((stages - 1) % C::kStages);
+                uint32_t okw = 1;
+                if (lane == 0) okw = mbar_wait_bounded(bar_tail + 8 * stage, (tails >> stage) & 1u, abort_flag, kWaitLimitNs) ? 1u : 0u;
+                okw = __shfl_sync(0xffffffffu, okw, 0);
+                if (!okw) {
+                    if (lane == 0) {
+                        *abort_flag = 1;
+                        atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+                    }
+                    break;
+                }
+                __syncwarp();
+                tails ^= 1u << stage;
+                const int slot = stage * C::kSub + (t.num_kt - 1) % C::kSub;
+                // 128-byte rows tail .. 63 of every 64-row box (the swizzle stays inside a row)
+                uint8_t* a = smem + C::kOffA + slot * C::kABytes;
+                uint8_t* b = smem + C::kOffB + slot * C::kBBytes;
+                const int pieces = (BK - t.tail) * 8;   // 16-byte pieces per box
+                for (int i = 0; i < BM / 64 + C::kBRows / 64; ++i) {
+                    uint8_t* box = i < BM / 64 ? a + i * 64 * kRowBytes : b + (i - BM / 64) * 64 * kRowBytes;
+                    uint4* p = reinterpret_cast<uint4*>(box + t.tail * kRowBytes);
+                    for (int j = lane; j < pieces; j += 32) p[j] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (NC == 2) mbar_arrive_cluster_release(lead_full + 8 * stage);
+                    else mbar_arrive(bar_full + 8 * stage);
+                }
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;                       // TMEM lane quarter this warp may access
+        const int half = (warp - kEpiWarp0) >> 2;     // column half of the 256-wide tile
+        const int row = q * 32 + lane;                // accumulator row owned by this thread
+        uint32_t acc_iter = 0;
+        // waits for accumulation acc_iter; false: a wait ran out somewhere
+        auto acquire = [&]() {
+            uint32_t okw = 1;
+            if (lane == 0)
+                okw = mbar_wait_bounded(bar_tmem_full + 8 * (acc_iter & 1u), (acc_iter >> 1) & 1u, abort_flag, kWaitLimitNs) ? 1u : 0u;
+            okw = __shfl_sync(0xffffffffu, okw, 0);
+            if (!okw && lane == 0) {
+                *abort_flag = 1;
+                atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+            }
+            __syncwarp();
+            tc_fence_after();
+            return okw != 0;
+        };
+        // the accumulator has been read (the loads completed at tcgen05.wait::ld; no memory
+        // written here is read by the MMA issuer, so the arrive needs no release)
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(lead_tmem_empty + 8 * (acc_iter & 1u));
+            ++acc_iter;
+        };
+        for (int64_t L = unit; L < total_tiles; L += num_units) {
+            const Tile t = get_tile<NC, kW>(g, table, L, rank);
+            const bool row_ok = row < t.valid_rows;
+            const int64_t col0 = t.n0 + half * 128;
+            const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+            if constexpr (kW) {
+                float sum[128];
+#pragma unroll
+                for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+                bool ok = true;
+                for (int kt = 0; kt < t.num_kt; kt += kPartSteps) {
+                    if (!(ok = acquire())) break;
+                    const uint32_t taddr = tmem_base + lanes + (acc_iter & 1u) * BN + half * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(taddr + c * 32, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
+                    }
+                    release();
+                }
+                if (!ok) break;
+                if (row_ok) {
+                    float* dst = static_cast<float*>(g.out) + (t.e * g.m_out + t.m_in + row) * g.n_out + col0;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (col0 + 8 * j < g.n_out) {
+                            const float* s = sum + 8 * j;
+                            if (g.wide_store) {
+                                st_global_v8(dst + 8 * j, __float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
+                                             __float_as_uint(s[3]), __float_as_uint(s[4]), __float_as_uint(s[5]),
+                                             __float_as_uint(s[6]), __float_as_uint(s[7]), l2_policy_evict_first());
+                            } else {
+                                reinterpret_cast<float4*>(dst)[2 * j] = make_float4(s[0], s[1], s[2], s[3]);
+                                reinterpret_cast<float4*>(dst)[2 * j + 1] = make_float4(s[4], s[5], s[6], s[7]);
+                            }
+                        }
+                    }
+                }
+            } else {
+                if (!acquire()) break;
+                const uint32_t taddr = tmem_base + lanes + (acc_iter & 1u) * BN + half * 128;
+                uint32_t w[64];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + c * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[c * 16 + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                }
+                release();
+                if (row_ok) {
+                    uint16_t* dst = static_cast<uint16_t*>(g.out) + (t.row0 + t.m_in + row) * g.n_out + col0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t* s = w + 8 * j;
+                        if (g.wide_store) {   // n_out % 16 == 0: 16 columns are all there or all past the end
+                            if (col0 + 16 * j < g.n_out)
+                                st_global_v8(dst + 16 * j, s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7],
+                                             l2_policy_evict_first());
+                        } else {
+                            if (col0 + 16 * j < g.n_out)
+                                reinterpret_cast<uint4*>(dst)[2 * j] = make_uint4(s[0], s[1], s[2], s[3]);
+                            if (col0 + 16 * j + 8 < g.n_out)
+                                reinterpret_cast<uint4*>(dst)[2 * j + 1] = make_uint4(s[4], s[5], s[6], s[7]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // both CTAs of a pair finish (and their copies drain) before TMEM is freed
+    tc_fence_before();
+    if (NC == 2) cluster_sync(); else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_g<NC>(tmem_base, kTmemCols);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (fn == nullptr) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
+}
+
+// Map of bf16 [outer x rows x cols] (outer = 1: a matrix) with boxes of 64 columns (128 bytes,
+// 128-byte swizzle) x box_rows rows; what lies outside reads as zero.
+bool make_map(CUtensorMap* m, const void* base, int64_t outer, int64_t rows, int64_t cols, int box_rows, bool three) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (enc == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * rows * 2};
+    cuuint32_t box[3] = {BK, static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, three ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Problem {
+    const void* A;
+    const void* B;
+    int64_t N, K;
+};
+
+template <int NC, int PASS>
+int launch_tiles(const Problem& pr, const Args& g, int dev, int num_sms, cudaStream_t stream) {
+    using C = Cfg<NC>;
+    constexpr bool kW = PASS == kBf16Wgrad;
+    static int units[64] = {0};   // co-resident units (CTAs or pairs), per device
+    auto kern = grouped_bf16_kernel<NC, PASS>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = NC;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (units[dev] == 0) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes)) !=
+            cudaSuccess)
+            return MX_ERR_CUDA;
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms / NC * NC), 1, 1);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = num_sms / NC;
+        units[dev] = n < num_sms / NC ? n : num_sms / NC;
+    }
+    CUtensorMap tmA, tmB;
+    const bool ok =
+        kW ? make_map(&tmA, pr.A, 1, g.R, pr.N, BK, false) && make_map(&tmB, pr.B, 1, g.R, pr.K, BK, false)
+        : PASS == kBf16Fwd
+            ? make_map(&tmA, pr.A, 1, g.R, pr.K, BM, false) && make_map(&tmB, pr.B, g.E, pr.N, pr.K, C::kBRows, true)
+            : make_map(&tmA, pr.A, 1, g.R, pr.K, BM, false) && make_map(&tmB, pr.B, g.E, pr.K, pr.N, BK, true);
+    if (!ok) return MX_ERR_CUDA;
+    // no more units than there can be tiles (the exact count lives on the device)
+    const int64_t mt = kW ? g.E * ceil_div(g.m_out, C::kTileM) : g.R / C::kTileM + (g.E < g.R ? g.E : g.R);
+    const int64_t tiles = mt * ceil_div(g.n_out, BN);
+    const int64_t grid = tiles < units[dev] ? tiles : units[dev];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid * NC), 1, 1);
+    return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, g) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32_t* off, int E, int64_t R, int64_t N,
                              int64_t K, void* out, int* dev_err, cudaStream_t stream) {
-    const int64_t mt = pass == kWgrad ? E * ceil_div(N, kTile) : R / kTile + E, nt = ceil_div(pass == kWgrad ? K : N, kTile);
-    if (mt > 65535 || nt >= (int64_t(1) << 31)) return MX_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(nt), static_cast<unsigned>(mt));
-    const auto* a = static_cast<const __nv_bfloat16*>(A);
-    const auto* b = static_cast<const __nv_bfloat16*>(B);
-    if (pass == kFwd) grouped_bf16_kernel<kFwd><<<grid, kThreads, 0, stream>>>(a, b, off, E, R, N, K, out, dev_err);
-    else if (pass == kDgrad) grouped_bf16_kernel<kDgrad><<<grid, kThreads, 0, stream>>>(a, b, off, E, R, N, K, out, dev_err);
-    else grouped_bf16_kernel<kWgrad><<<grid, kThreads, 0, stream>>>(a, b, off, E, R, N, K, out, dev_err);
-    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+    int dev = 0;
+    static int num_sms[64] = {0};
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MX_ERR_CUDA;
+    if (num_sms[dev] == 0 &&
+        (cudaDeviceGetAttribute(&num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || num_sms[dev] <= 0))
+        return MX_ERR_CUDA;
+    const bool w = pass == kBf16Wgrad;
+    Args g;
+    g.off = off;
+    g.E = E;
+    g.R = R;
+    g.m_out = w ? N : 0;
+    g.n_out = w ? K : N;
+    g.k_len = w ? 0 : K;
+    g.out = out;
+    g.wide_store = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && (w || N % 16 == 0) ? 1 : 0;
+    g.dev_err = dev_err;
+    const Problem pr{A, B, N, K};
+    const int n = num_sms[dev];
+    const bool pairs = w ? N > BM : R / E >= 512;
+    if (pass == kBf16Fwd)
+        return pairs ? launch_tiles<2, kBf16Fwd>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Fwd>(pr, g, dev, n, stream);
+    if (pass == kBf16Dgrad)
+        return pairs ? launch_tiles<2, kBf16Dgrad>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Dgrad>(pr, g, dev, n, stream);
+    return pairs ? launch_tiles<2, kBf16Wgrad>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Wgrad>(pr, g, dev, n, stream);
 }
 
 }  // namespace mx
