@@ -30,8 +30,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                        // consecutive elements of a thread
-constexpr int kChunk = kThreads * kPer;        // elements of a chunk: the unit a CTA works on
-constexpr int kNormCtas = 1216;                // most CTAs of the norm: 8 on each of 152 SMs
+constexpr int kGroup = kThreads * kPer;        // elements that a CTA takes in one go
+constexpr int kChunk = 2 * kGroup;             // elements of a chunk: what a CTA does for one look at the plan
+constexpr int kStepCtas32 = 4, kStepCtas8 = 4; // CTAs of the step on an SM (64 and 80 registers a thread)
+constexpr int kNormCtasPerSm = 5;
+constexpr int kNormCtas = 1024;                // most CTAs of the norm
 
 // One tensor of the plan in device memory.
 struct Slot {
@@ -46,8 +49,17 @@ struct Slot {
     int64_t chunk0;     // first chunk of the tensor in the plan
     int64_t pos0;       // position of its first element: tensors start at multiples of 32
     float wd, lr_mult;
-    int32_t p_f32, g_f32;
+    int32_t flags, unused;
 };
+static_assert(sizeof(Slot) == 96, "six 16-byte loads");
+__device__ __forceinline__ Slot load_slot(const Slot* s) {
+    union { Slot s; uint4 q[6]; } u;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) u.q[i] = __ldg(reinterpret_cast<const uint4*>(s) + i);
+    return u.s;
+}
+constexpr int kParamF32 = 1, kGradF32 = 2;
+constexpr int kWide = 4;   // every fp32 tensor of the slot starts on a 32-byte boundary
 
 // The plan: header, slots, then for every chunk the index of its tensor.
 struct Header {
@@ -85,25 +97,40 @@ __device__ __forceinline__ uint32_t step_key(uint32_t seed, int64_t t) {
     return mix(seed + 0x9E3779B9u * static_cast<uint32_t>(t)) ^ static_cast<uint32_t>(static_cast<uint64_t>(t) >> 32);
 }
 
-// ------------------------------------------------------------------ values of 8 elements
-struct Vals {
-    float x[kPer];
-};
+// ------------------------------------------------------------------ 8 elements in memory
+// Streaming loads of memory that the same thread writes later on (so not through the read-only path).
+__device__ __forceinline__ uint4 ld_own_16(const void* p) {
+    uint4 v;
+    asm("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void ld_own_32(const void* p, uint32_t* w) {
+    asm("ld.global.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+}
 
-__device__ __forceinline__ void load_f32(const float* src, int valid, float (&x)[kPer]) {
+__device__ __forceinline__ void load_f32(const float* src, int valid, bool wide, float (&x)[kPer]) {
+    uint32_t w[kPer];
     if (valid == kPer) {
-        const uint4 a = *reinterpret_cast<const uint4*>(src), b = *reinterpret_cast<const uint4*>(src + 4);
-        x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
-        x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+        if (wide) {
+            ld_own_32(src, w);
+        } else {
+            const uint4 a = ld_own_16(src), b = ld_own_16(src + 4);
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x[i] = i < valid ? src[i] : 0.f;
+        for (int i = 0; i < kPer; ++i) w[i] = i < valid ? __float_as_uint(src[i]) : 0u;
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = __uint_as_float(w[i]);
 }
 
 __device__ __forceinline__ void load_bf16(const uint16_t* src, int valid, float (&x)[kPer]) {
     if (valid == kPer) {
-        const uint4 a = *reinterpret_cast<const uint4*>(src);
+        const uint4 a = ld_own_16(src);
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -116,10 +143,17 @@ __device__ __forceinline__ void load_bf16(const uint16_t* src, int valid, float 
     }
 }
 
-__device__ __forceinline__ void store_f32(float* dst, int valid, const float (&x)[kPer]) {
+__device__ __forceinline__ void store_f32(float* dst, int valid, bool wide, const float (&x)[kPer]) {
     if (valid == kPer) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        if (wide) {
+            uint32_t w[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) w[i] = __float_as_uint(x[i]);
+            st_global_32(dst, w);
+        } else {
+            reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
@@ -139,9 +173,7 @@ __device__ __forceinline__ void store_words(uint16_t* dst, int valid, const uint
 
 __device__ __forceinline__ void load_bytes(const uint8_t* src, int valid, uint32_t (&w)[2]) {
     if (valid == kPer) {
-        const uint2 a = *reinterpret_cast<const uint2*>(src);
-        w[0] = a.x;
-        w[1] = a.y;
+        asm("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(src));
     } else {
         w[0] = w[1] = 0;
 #pragma unroll
@@ -160,48 +192,45 @@ __device__ __forceinline__ void store_bytes(uint8_t* dst, int valid, const uint3
     }
 }
 
-__device__ __forceinline__ void load_any(const void* base, bool f32, int64_t at, int valid, float (&x)[kPer]) {
-    if (f32) load_f32(static_cast<const float*>(base) + at, valid, x);
+__device__ __forceinline__ void load_any(const void* base, bool f32, int64_t at, int valid, bool wide, float (&x)[kPer]) {
+    if (f32) load_f32(static_cast<const float*>(base) + at, valid, wide, x);
     else load_bf16(static_cast<const uint16_t*>(base) + at, valid, x);
 }
 
 // ------------------------------------------------------------------ 8-bit states
-// 2^(b - 127); 0 for b = 0 (a block of zeros), Inf for b = 0xFF (times a NaN or zero code: NaN)
-__device__ __forceinline__ float scale_value(uint32_t b) { return __uint_as_float(b << 23); }
+// 2^(b - 127); 0 for b = 0 (a block of zeros), NaN for b = 0xFF
+__device__ __forceinline__ float scale_value(uint32_t b) {
+    return b == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 23);
+}
 
-__device__ __forceinline__ void decode_m(const uint32_t (&w)[2], uint32_t b, float (&x)[kPer]) {
-    const float s = scale_value(b);
+// E4M3 codes as pairs of fp32, without their block's scale
+__device__ __forceinline__ void decode_m(const uint32_t (&w)[2], uint64_t (&x)[kPer / 2]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint16_t two = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
         uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
         float lo, hi;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
             : "=f"(lo), "=f"(hi) : "r"(h));
-        x[2 * i] = lo * s;
-        x[2 * i + 1] = hi * s;
+        x[i] = pk2(lo, hi);
     }
 }
 
-__device__ __forceinline__ void decode_r(const uint32_t (&w)[2], uint32_t b, float (&x)[kPer]) {
-    const float s = scale_value(b);
+// Codes of r as pairs of fp32, without their block's scale.  NONZERO: no code is 0.
+template <bool NONZERO>
+__device__ __forceinline__ void decode_r(const uint32_t (&w)[2], uint64_t (&x)[kPer / 2]) {
+    float f[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const uint32_t c = (w[i / 4] >> (8 * (i & 3))) & 0xFFu;
-        x[i] = (c != 0 ? __uint_as_float((c << 19) + (112u << 23)) : 0.f) * s;
+        const uint32_t c = __byte_perm(w[i / 4], 0u, 0x4044u | ((i & 3u) << 8));   // the code in byte 2
+        f[i] = NONZERO || c != 0 ? __uint_as_float(c * 8u + (112u << 23)) : 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pk2(f[2 * i], f[2 * i + 1]);
 }
 
-// Largest of the 32 elements' magnitude bits: 8 of this thread, 8 of each of its three neighbours.
-// As integers NaN > Inf > every finite value, so none is lost.
-__device__ __forceinline__ uint32_t block_amax(const float (&x)[kPer]) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-}
+__device__ __forceinline__ bool has_zero_byte(uint32_t w) { return ((w - 0x01010101u) & ~w & 0x80808080u) != 0; }
 
 // Scale byte for a block whose largest magnitude has the bits a: exponent minus `shift`, one more
 // where the mantissa passes `over` (the code's largest one).  1 at least for a block with a
@@ -213,38 +242,111 @@ __device__ __forceinline__ uint32_t block_byte(uint32_t a, int shift, uint32_t o
     return b < 1 ? 1u : static_cast<uint32_t>(b);
 }
 
-// E4M3 codes of x / 2^(b - 127), stochastically rounded by 16 bits of u each: the 20 bits below
-// the code's 3 mantissa bits are filled up by u, then cut.  Below 2^-6 the code's grid is 2^-9
-// throughout; adding 2^-6 first gives fp32 that grid.
-__device__ __forceinline__ void encode_m(const float (&x)[kPer], uint32_t b, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
-    if (b == 0xFFu) {
-        w[0] = w[1] = 0x7F7F7F7Fu;
-        return;
+// Largest magnitude's bits over the block's four threads.  As integers NaN > Inf > every finite
+// value, so none is lost.
+__device__ __forceinline__ uint32_t block_max(uint32_t a) {
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+__device__ __forceinline__ float inv_block(uint32_t b) { return __uint_as_float((254u - (b == 0 ? 1u : b)) << 23); }
+
+constexpr float kSmallestNormal = 0.015625f;              // E4M3: 2^-6
+constexpr float kSmallestRoot = 1.0625f / 32768.0f;       // code 1 of r
+
+// max / min of three magnitudes; NaN comes through
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max8(const float (&x)[kPer]) {
+    return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
+}
+__device__ __forceinline__ float min8(const float (&x)[kPer]) {
+    return min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min3(x[6], x[7], x[7]));
+}
+__device__ __forceinline__ void unpack8(const uint64_t (&x)[kPer / 2], float (&f)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+        f[2 * i] = lo2(x[i]);
+        f[2 * i + 1] = hi2(x[i]);
     }
-    const float inv = __uint_as_float((254u - (b == 0 ? 1u : b)) << 23);
+}
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t (&c)[4]) {
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+}
+
+// E4M3 codes of x / 2^(b - 127), stochastically rounded by 16 bits of u each: the 20 bits below
+// the code's 3 mantissa bits are filled up by u, then cut.
+// The short form, for a block whose every |x| is E4M3-normal under the scale (2^-6 at least): the
+// rounded fp32's exponent and mantissa, rebiased by 120, are the code's low 7 bits; multiplying by
+// 16 brings them to the top byte, where 0x40 completes the rebias (-120 * 2^27 = 2^30 mod 2^32).
+__device__ __forceinline__ void encode_m_short(const uint64_t (&m)[kPer / 2], float inv, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
+    uint64_t y2[kPer / 2];
+    float y[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) y2[i] = mul2(m[i], pk2(inv, inv));
+    unpack8(y2, y);
+    uint32_t c[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t bits = __float_as_uint(y[i]);
+        c[i] = (bits * 16u + __byte_perm(u[i], 0x40000000u, 0x7324)) | (bits & 0x80000000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t q[4] = {c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
+        w[i] = top_bytes(q);
+    }
+}
+// The form for every block.  Below 2^-6 the code's grid is 2^-9 throughout; adding 2^-6 of the
+// same sign first gives fp32 that grid.
+__device__ __forceinline__ void encode_m_any(const float (&m)[kPer], uint32_t b, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
+    const float inv = inv_block(b);
     float q[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        float y = fabsf(x[i]) * inv;
-        const bool small = y < 0.015625f;
-        if (small) y += 0.015625f;
-        y = __uint_as_float((__float_as_uint(y) + ((u[i] >> 16) << 4)) & ~0xFFFFFu);
-        if (small) y -= 0.015625f;
-        q[i] = copysignf(y, x[i]);
+        float y = m[i] * inv;
+        const float lift = fabsf(y) < kSmallestNormal ? copysignf(kSmallestNormal, y) : 0.f;
+        y = __uint_as_float((__float_as_uint(y + lift) + ((u[i] >> 12) & 0xFFFF0u)) & ~0xFFFFFu);
+        q[i] = copysignf(y - lift, m[i]);
     }
-    w[0] = cvt_e4m3x4(q[0], q[1], q[2], q[3]);
-    w[1] = cvt_e4m3x4(q[4], q[5], q[6], q[7]);
+    w[0] = b == 0xFFu ? 0x7F7F7F7Fu : cvt_e4m3x4(q[0], q[1], q[2], q[3]);
+    w[1] = b == 0xFFu ? 0x7F7F7F7Fu : cvt_e4m3x4(q[4], q[5], q[6], q[7]);
 }
 
-__device__ __forceinline__ void encode_r(const float (&r)[kPer], uint32_t b, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
+// Codes of r / 2^(b - 127): the 19 bits below the code's 4 mantissa bits filled up by u, then cut.
+// The short form, for a block whose every r is at least the smallest code's value: exponent and
+// mantissa, rebiased by 112, are the code; multiplied by 32 it is the top byte (112 * 2^28 = 0
+// mod 2^32).
+__device__ __forceinline__ void encode_r_short(const float (&r)[kPer], float inv, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
+    uint32_t c[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+        const uint64_t y = mul2(pk2(r[2 * i], r[2 * i + 1]), pk2(inv, inv));
+        c[2 * i] = __float_as_uint(lo2(y)) * 32u + __byte_perm(u[2 * i], 0u, 0x4104);
+        c[2 * i + 1] = __float_as_uint(hi2(y)) * 32u + __byte_perm(u[2 * i + 1], 0u, 0x4104);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t q[4] = {c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]};
+        w[i] = top_bytes(q);
+    }
+}
+__device__ __forceinline__ void encode_r_any(const float (&r)[kPer], uint32_t b, const uint32_t (&u)[kPer], uint32_t (&w)[2]) {
+    const float inv = inv_block(b);
     w[0] = w[1] = 0;
-    if (b == 0xFFu) return;
-    const float inv = __uint_as_float((254u - (b == 0 ? 1u : b)) << 23);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const uint32_t bits = __float_as_uint(r[i] * inv) + ((u[i] & 0xFFFFu) << 3);
-        const int c = static_cast<int>(bits >> 19) - (112 << 4);
-        w[i / 4] |= (r[i] > 0.f ? static_cast<uint32_t>(c < 1 ? 1 : c) : 0u) << (8 * (i & 3));
+        const int bits = static_cast<int>(__float_as_uint(r[i] * inv) + ((u[i] & 0xFFFFu) << 3));
+        const uint32_t c = static_cast<uint32_t>(max((bits >> 19) - (112 << 4), 1));
+        if (r[i] > 0.f && b != 0xFFu) w[i / 4] |= c << (8 * (i & 3));
     }
 }
 
@@ -255,104 +357,241 @@ struct StepArgs {
     int64_t* step;
     double log_b1, log_b2;   // ln b1, ln b2
     float lr, b1, c1, b2, c2, eps;   // c1 = 1 - b1, c2 = 1 - b2, each rounded from 64 bits
+    float root_b2, root_c2;
     const float* lr_dev;
     const float* grad_scale;
     uint32_t seed;
     int stochastic;
 };
 
+// Square roots and quotients come from the special-function unit, within 2^-22 relative: they
+// form an update that is a small part of the parameter, or codes of 5 bits.  (ftz: a subnormal
+// v has root 0.)
+__device__ __forceinline__ float root(float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float root_ftz(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// bf16 words of the parameters, rounded stochastically by 16 further bits each.  SAFE: NaN, whose
+// bits could carry over into the sign, is kept apart.  (Inf plus 16 bits below the cut stays Inf.)
+template <bool SAFE>
+__device__ __forceinline__ void round_params(const float (&p)[kPer], const uint32_t (&u)[kPer], uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t x = u[2 * i + j];
+            const uint32_t y = (x ^ (x >> 7)) * 0xC2B2AE3Du;
+            h[j] = __float_as_uint(p[2 * i + j]) + (y >> 16);
+            if (SAFE && isnan(p[2 * i + j])) h[j] = 0x7FC00000u;
+        }
+        w[i] = __byte_perm(h[0], h[1], 0x7632);
+    }
+}
+__device__ __forceinline__ void nearest_params(const float (&p)[kPer], uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+}
+
+// p (1 - lr wd) - lr_t m / (r inv_v + eps), p rounded once; the denominator is normal (eps >= 1e-30)
+struct Rate {
+    float keep, neg_lr_t, inv_v, eps;
+};
+__device__ __forceinline__ float updated(float p, float m, float r, const Rate& k) {
+    return fmaf(p, k.keep, k.neg_lr_t * m * rcp_approx_ftz(fmaf(r, k.inv_v, k.eps)));
+}
+
+// What one thread brings of 8 elements.
+struct Raw8 {
+    float p[kPer], g[kPer];
+    uint32_t m[2], r[2], sm, sr;
+};
+
+__device__ __forceinline__ int valid_of(int64_t n, int64_t at) {
+    const int64_t left = n - at;
+    return left >= kPer ? kPer : (left > 0 ? static_cast<int>(left) : 0);
+}
+
+__device__ __forceinline__ void load8(const Slot& sl, int64_t at, int valid, Raw8& x) {
+    load_bytes(static_cast<const uint8_t*>(sl.m) + at, valid, x.m);
+    load_bytes(static_cast<const uint8_t*>(sl.v) + at, valid, x.r);
+    x.sm = x.sr = 0;
+    if (valid > 0) {
+        asm("ld.global.u8 %0, [%1];" : "=r"(x.sm) : "l"(sl.sm + at / 32));
+        asm("ld.global.u8 %0, [%1];" : "=r"(x.sr) : "l"(sl.sr + at / 32));
+    }
+    load_any(sl.g, (sl.flags & kGradF32) != 0, at, valid, (sl.flags & kWide) != 0, x.g);
+    load_any(sl.p, (sl.flags & kParamF32) != 0, at, valid, (sl.flags & kWide) != 0, x.p);
+}
+
+// The step on 8 elements with 8-bit moments.  Scales and factors fold into one:
+//   m = (b1 s_m) q + (c1 gs) g,   v = (root(b2) s_r q)^2 + (root(c2) gs g)^2
+// in packed pairs.  The short forms serve a warp whose blocks hold no zero, subnormal, NaN or Inf
+// and no m below E4M3's normal range under its scale -- all but a few of the warps of a weight's
+// gradient; any other warp takes the long ones.  Bound by instructions: 119 a thread's element
+// with IEEE square root and quotient and branches per element, 83 without them, about 50 with
+// packed arithmetic and the short codes.
+__device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw8& x, const StepArgs& a, float gs,
+                                      const Rate& k, uint32_t pos_lo, uint32_t key) {
+    const bool p_f32 = (sl.flags & kParamF32) != 0;
+    const bool sr_p = a.stochastic && !p_f32;
+    uint32_t u[kPer], wp[4], wm[2], wr[2];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) u[i] = mix((pos_lo ^ key) ^ i);   // (pos_lo is a multiple of 8)
+    const float fm = a.b1 * scale_value(x.sm), fr = a.root_b2 * scale_value(x.sr), gm = a.c1 * gs, gv = a.root_c2 * gs;
+    uint64_t m2[kPer / 2], q[kPer / 2], r2[kPer / 2];
+    decode_m(x.m, q);
+    if (has_zero_byte(x.r[0]) || has_zero_byte(x.r[1])) decode_r<false>(x.r, r2);
+    else decode_r<true>(x.r, r2);
+    float m[kPer], v[kPer], r[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+        const uint64_t g2 = pk2(x.g[2 * i], x.g[2 * i + 1]);
+        m2[i] = fma2(pk2(fm, fm), q[i], mul2(pk2(gm, gm), g2));
+        const uint64_t old = mul2(pk2(fr, fr), r2[i]), add = mul2(pk2(gv, gv), g2);
+        r2[i] = fma2(old, old, mul2(add, add));
+    }
+    unpack8(m2, m);
+    unpack8(r2, v);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r[i] = root_ftz(v[i]);
+    const uint32_t bm = block_byte(block_max(__float_as_uint(max8(m))), 8, 0x600000u);
+    uint32_t br = block_byte(block_max(__float_as_uint(max8(r))), 0, 0x780000u);
+    const float im = inv_block(bm), ir = inv_block(br);
+    const uint64_t ps = add2(add2(pk2(x.p[0], x.p[1]), pk2(x.p[2], x.p[3])), add2(pk2(x.p[4], x.p[5]), pk2(x.p[6], x.p[7])));
+    const bool plain = bm != 0xFFu && br != 0xFFu && min8(m) * im >= kSmallestNormal && min8(r) * ir >= kSmallestRoot &&
+                       fabsf(lo2(ps) + hi2(ps)) < __uint_as_float(0x7F800000u);
+    if (__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) {
+            const uint64_t den = fma2(pk2(r[2 * i], r[2 * i + 1]), pk2(k.inv_v, k.inv_v), pk2(k.eps, k.eps));
+            const uint64_t inv = pk2(rcp_approx_ftz(lo2(den)), rcp_approx_ftz(hi2(den)));
+            const uint64_t up = mul2(mul2(pk2(k.neg_lr_t, k.neg_lr_t), m2[i]), inv);
+            const uint64_t p2 = fma2(pk2(x.p[2 * i], x.p[2 * i + 1]), pk2(k.keep, k.keep), up);
+            x.p[2 * i] = lo2(p2);
+            x.p[2 * i + 1] = hi2(p2);
+        }
+        encode_m_short(m2, im, u, wm);
+        encode_r_short(r, ir, u, wr);
+        if (sr_p) round_params<false>(x.p, u, wp);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            r[i] = root(v[i]);
+            x.p[i] = updated(x.p[i], m[i], r[i], k);
+        }
+        br = block_byte(block_max(__float_as_uint(max8(r))), 0, 0x780000u);
+        encode_m_any(m, bm, u, wm);
+        encode_r_any(r, br, u, wr);
+        if (sr_p) round_params<true>(x.p, u, wp);
+    }
+    store_bytes(static_cast<uint8_t*>(sl.m) + at, valid, wm);
+    store_bytes(static_cast<uint8_t*>(sl.v) + at, valid, wr);
+    if ((threadIdx.x & 3) == 0 && valid > 0) {
+        sl.sm[at / 32] = static_cast<uint8_t>(bm);
+        sl.sr[at / 32] = static_cast<uint8_t>(br);
+    }
+    if (!sr_p) nearest_params(x.p, wp);
+    if (p_f32) store_f32(static_cast<float*>(sl.p) + at, valid, (sl.flags & kWide) != 0, x.p);
+    else store_words(static_cast<uint16_t*>(sl.p) + at, valid, wp);
+    if (sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
+}
+
+// The step on 8 elements with fp32 moments.  Bound by HBM: 24 to 30 bytes an element.
+__device__ __forceinline__ void step32(const Slot& sl, int64_t at, int valid, const StepArgs& a, float gs, const Rate& k,
+                                       uint32_t pos_lo, uint32_t key) {
+    const bool p_f32 = (sl.flags & kParamF32) != 0, wide = (sl.flags & kWide) != 0;
+    float p[kPer], g[kPer], m[kPer], v[kPer];
+    uint32_t wp[4];
+    load_f32(static_cast<const float*>(sl.m) + at, valid, wide, m);
+    load_f32(static_cast<const float*>(sl.v) + at, valid, wide, v);
+    load_any(sl.g, (sl.flags & kGradF32) != 0, at, valid, wide, g);
+    load_any(sl.p, p_f32, at, valid, wide, p);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const float x = g[i] * gs;
+        m[i] = fmaf(a.b1, m[i], a.c1 * x);
+        v[i] = fmaf(a.b2, v[i], a.c2 * x * x);
+        p[i] = updated(p[i], m[i], root(v[i]), k);
+    }
+    store_f32(static_cast<float*>(sl.m) + at, valid, wide, m);
+    store_f32(static_cast<float*>(sl.v) + at, valid, wide, v);
+    if (a.stochastic && !p_f32) {
+        uint32_t u[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) u[i] = mix((pos_lo ^ key) ^ i);
+        round_params<true>(p, u, wp);
+    } else {
+        nearest_params(p, wp);
+    }
+    if (p_f32) store_f32(static_cast<float*>(sl.p) + at, valid, wide, p);
+    else store_words(static_cast<uint16_t*>(sl.p) + at, valid, wp);
+    if (sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
+}
+
 template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads) adamw_step_kernel(void* plan, const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, EIGHT ? kStepCtas8 : kStepCtas32) adamw_step_kernel(void* plan, const StepArgs a) {
     const PlanView pv = view(plan, a.n);
     __shared__ float s_bc[2];
     const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
     const int64_t t = *a.step + 1;
     if (!isfinite(gs)) return;   // the gradients were not finite: the step is skipped, t stays
     if (threadIdx.x == 0) {
-        s_bc[0] = -expm1f(static_cast<float>(static_cast<double>(t) * a.log_b1));            // 1 - b1^t
+        s_bc[0] = 1.0f / -expm1f(static_cast<float>(static_cast<double>(t) * a.log_b1));     // 1 / (1 - b1^t)
         s_bc[1] = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(t) * a.log_b2)));   // (1 - b2^t)^-1/2
     }
     __syncthreads();
-    const int64_t chunk = blockIdx.x;
-    const Slot& sl = pv.slots[pv.of_chunk[chunk]];
-    const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
-    const int64_t left = sl.n - at;
-    const int valid = left >= kPer ? kPer : (left > 0 ? static_cast<int>(left) : 0);
-    const float lr = (a.lr_dev != nullptr ? *a.lr_dev : a.lr) * sl.lr_mult;
-    const float keep = 1.0f - lr * sl.wd, lr_t = lr / s_bc[0], inv_v = s_bc[1];
-    float p[kPer], g[kPer], m[kPer], v[kPer], r[kPer];
-    uint32_t wm[2], wr[2];
-    load_any(sl.p, sl.p_f32, at, valid, p);
-    load_any(sl.g, sl.g_f32, at, valid, g);
-    if (EIGHT) {
-        load_bytes(static_cast<const uint8_t*>(sl.m) + at, valid, wm);
-        load_bytes(static_cast<const uint8_t*>(sl.v) + at, valid, wr);
-        decode_m(wm, valid > 0 ? sl.sm[at / 32] : 0u, m);
-        decode_r(wr, valid > 0 ? sl.sr[at / 32] : 0u, r);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = r[i] * r[i];
-    } else {
-        load_f32(static_cast<const float*>(sl.m) + at, valid, m);
-        load_f32(static_cast<const float*>(sl.v) + at, valid, v);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const float x = g[i] * gs;
-        m[i] = fmaf(a.b1, m[i], a.c1 * x);
-        v[i] = fmaf(a.b2, v[i], a.c2 * x * x);
-        r[i] = sqrtf(v[i]);
-        p[i] = fmaf(p[i], keep, -lr_t * (m[i] / fmaf(r[i], inv_v, a.eps)));
-    }
-    const bool sr_p = a.stochastic && !sl.p_f32;
-    uint32_t u[kPer];
-    if (EIGHT || sr_p) {
+    const float lr0 = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+    const float inv_bc1 = s_bc[0];
+    Rate k;
+    k.inv_v = s_bc[1];
+    k.eps = a.eps;
+    const uint32_t key0 = step_key(a.seed, t);
+    // a run of consecutive chunks for every CTA, so that the tensor rarely changes
+    const int64_t c0 = a.chunks * blockIdx.x / gridDim.x, c1 = a.chunks * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t chunk = c0; chunk < c1; ++chunk) {
+        const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
+        const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
+        const int v0 = valid_of(sl.n, at), v1 = valid_of(sl.n, at + kGroup);
+        // the tensor's next chunk on its way into L2 during this one's arithmetic
+        if (EIGHT && threadIdx.x < 4 && chunk + 1 < c1) {
+            const int64_t nx = (chunk + 1 - sl.chunk0) * kChunk;
+            int64_t cnt = sl.n - nx;
+            cnt = cnt > kChunk ? kChunk : cnt;
+            const int sh = threadIdx.x == 0 ? ((sl.flags & kGradF32) ? 2 : 1) : threadIdx.x == 1 ? ((sl.flags & kParamF32) ? 2 : 1) : 0;
+            const char* base = static_cast<const char*>(threadIdx.x == 0 ? sl.g : threadIdx.x == 1 ? sl.p : threadIdx.x == 2 ? sl.m : sl.v);
+            const int64_t bytes = cnt * (1 << sh) & ~int64_t(15);
+            if (bytes > 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(base + nx * (1 << sh)), "r"(static_cast<uint32_t>(bytes)));
+        }
+        const float lr = lr0 * sl.lr_mult;
+        k.keep = 1.0f - lr * sl.wd;
+        k.neg_lr_t = -lr * inv_bc1;
         const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
-        const uint32_t key = mix(step_key(a.seed, t) + static_cast<uint32_t>(pos >> 32));
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) u[i] = mix((static_cast<uint32_t>(pos) + i) ^ key);
-    }
-    if (sl.p_f32) {
-        store_f32(static_cast<float*>(sl.p) + at, valid, p);
-        if (sl.copy != nullptr) {
-            const uint32_t w[4] = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
-            store_words(static_cast<uint16_t*>(sl.copy) + at, valid, w);
-        }
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (sr_p) {
-                uint32_t h[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t x = u[2 * i + j];
-                    const uint32_t y = ((x ^ (x >> 7)) * 0xC2B2AE3Du) >> 16;
-                    const uint32_t bits = __float_as_uint(p[2 * i + j]);
-                    h[j] = (bits & 0x7F800000u) == 0x7F800000u ? bits | ((bits & 0x7FFFFFu) != 0 ? 0x400000u : 0u) : bits + y;
-                }
-                w[i] = __byte_perm(h[0], h[1], 0x7632);
-            } else {
-                w[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+        const uint32_t key = mix(key0 + static_cast<uint32_t>(pos >> 32));
+        const uint64_t pos1 = pos + kGroup;
+        const uint32_t key1 = mix(key0 + static_cast<uint32_t>(pos1 >> 32));
+        if (EIGHT) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                Raw8 x;
+                const int vv = h ? v1 : v0;
+                load8(sl, at + h * kGroup, vv, x);
+                step8(sl, at + h * kGroup, vv, x, a, gs, k, static_cast<uint32_t>(h ? pos1 : pos), h ? key1 : key);
             }
+        } else {
+            step32(sl, at, v0, a, gs, k, static_cast<uint32_t>(pos), key);
+            step32(sl, at + kGroup, v1, a, gs, k, static_cast<uint32_t>(pos1), key1);
         }
-        store_words(static_cast<uint16_t*>(sl.p) + at, valid, w);
-    }
-    if (EIGHT) {
-        const uint32_t bm = block_byte(block_amax(m), 8, 0x600000u), br = block_byte(block_amax(r), 0, 0x780000u);
-        encode_m(m, bm, u, wm);
-        encode_r(r, br, u, wr);
-        store_bytes(static_cast<uint8_t*>(sl.m) + at, valid, wm);
-        store_bytes(static_cast<uint8_t*>(sl.v) + at, valid, wr);
-        if ((threadIdx.x & 3) == 0 && valid > 0) {
-            sl.sm[at / 32] = static_cast<uint8_t>(bm);
-            sl.sr[at / 32] = static_cast<uint8_t>(br);
-        }
-    } else {
-        store_f32(static_cast<float*>(sl.m) + at, valid, m);
-        store_f32(static_cast<float*>(sl.v) + at, valid, v);
     }
     // every CTA has read the step by now: the last to arrive here counts it
-    __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         if (atomicAdd(&pv.h->step_done, 1u) == gridDim.x - 1) {
@@ -363,24 +602,32 @@ __global__ void __launch_bounds__(kThreads) adamw_step_kernel(void* plan, const 
 }
 
 // ------------------------------------------------------------------ the gradient norm
-// Squares are summed in fp32 over a thread's 8 elements of a chunk and in 64 bits above that, in a
-// fixed order: per thread over its chunks, per warp and CTA by a tree, over the CTAs in order.
-__global__ void __launch_bounds__(kThreads) adamw_norm_kernel(void* plan, int n, int64_t chunks, float max_norm,
+// Squares are summed in fp32 over a thread's 16 elements of 2 chunks and in 64 bits above that, in
+// a fixed order: per thread over its chunks, per warp and CTA by a tree, over the CTAs in order.
+__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) adamw_norm_kernel(void* plan, int n, int64_t chunks, float max_norm,
                                                               float* out) {
     const PlanView pv = view(plan, n);
     __shared__ double s_sum[kThreads / 32];
     __shared__ bool s_last;
     double sum = 0.0;
-    for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-        const Slot& sl = pv.slots[pv.of_chunk[chunk]];
-        const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
-        const int64_t left = sl.n - at;
-        const int valid = left >= kPer ? kPer : (left > 0 ? static_cast<int>(left) : 0);
-        float g[kPer];
-        load_any(sl.g, sl.g_f32, at, valid, g);
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t chunk = c0; chunk < c1; chunk += 2) {
+        float g[4][kPer];   // two groups each of two chunks
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bool in = chunk + k / 2 < c1;
+            const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + (in ? chunk + k / 2 : chunk)));
+            const int64_t at = (chunk + k / 2 - sl.chunk0) * kChunk + (k & 1) * kGroup + threadIdx.x * kPer;
+            load_any(sl.g, (sl.flags & kGradF32) != 0, at, in ? valid_of(sl.n, at) : 0, (sl.flags & kWide) != 0, g[k]);
+        }
         float part = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) part = fmaf(g[i], g[i], part);
+        for (int k = 0; k < 4; ++k) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) s = fmaf(g[k][i], g[k][i], s);
+            part += s;
+        }
         sum += static_cast<double>(part);
     }
     auto block_sum = [&](double x) {
@@ -420,20 +667,30 @@ __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(void* plan, int n,
 __global__ void __launch_bounds__(kThreads) adamw_values_kernel(void* plan, int n, uint16_t* mom, uint16_t* root) {
     const PlanView pv = view(plan, n);
     const int64_t chunk = blockIdx.x;
-    const Slot& sl = pv.slots[pv.of_chunk[chunk]];
-    const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
-    const int64_t left = sl.n - at;
-    const int valid = left >= kPer ? kPer : (left > 0 ? static_cast<int>(left) : 0);
-    if (valid == 0) return;
-    uint32_t w[2];
-    float x[kPer];
+    const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
+    const int64_t at0 = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
+    uint32_t w[4][2];
+    float s[4];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        load_bytes(static_cast<const uint8_t*>(which ? sl.v : sl.m) + at, valid, w);
-        if (which) decode_r(w, sl.sr[at / 32], x);
-        else decode_m(w, sl.sm[at / 32], x);
-        const uint32_t o[4] = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-        store_words((which ? root : mom) + sl.pos0 + at, valid, o);
+    for (int k = 0; k < 4; ++k) {   // two groups, m and r of each
+        const int64_t at = at0 + k / 2 * kGroup;
+        const int valid = valid_of(sl.n, at);
+        load_bytes(static_cast<const uint8_t*>(k & 1 ? sl.v : sl.m) + at, valid, w[k]);
+        s[k] = valid > 0 ? scale_value((k & 1 ? sl.sr : sl.sm)[at / 32]) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t at = at0 + k / 2 * kGroup;
+        uint64_t x[kPer / 2];
+        if (k & 1) decode_r<false>(w[k], x);
+        else decode_m(w[k], x);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = mul2(x[i], pk2(s[k], s[k]));
+            o[i] = pack_bf16x2(lo2(x[i]), hi2(x[i]));
+        }
+        store_words((k & 1 ? root : mom) + sl.pos0 + at, valid_of(sl.n, at), o);
     }
 }
 
@@ -483,8 +740,13 @@ int build_adamw_plan(const adamw_tensor* tensors, int n, int state_bits, void* i
     chunks = pos = 0;
     for (int i = 0; i < n; ++i) {
         const adamw_tensor& x = tensors[i];
+        const uintptr_t f32s = (x.param_dtype == MX_DTYPE_F32 ? reinterpret_cast<uintptr_t>(x.param) : 0) |
+                               (x.grad_dtype == MX_DTYPE_F32 ? reinterpret_cast<uintptr_t>(x.grad) : 0) |
+                               (eight ? 0 : reinterpret_cast<uintptr_t>(x.moment) | reinterpret_cast<uintptr_t>(x.second));
+        const int flags = (x.param_dtype == MX_DTYPE_F32 ? kParamF32 : 0) | (x.grad_dtype == MX_DTYPE_F32 ? kGradF32 : 0) |
+                          ((f32s & 31u) == 0 ? kWide : 0);
         slots[i] = Slot{x.param, x.grad, x.moment, x.second, x.scale_m, x.scale_r, x.copy, x.n, chunks, pos, x.weight_decay,
-                        x.lr_mult, x.param_dtype == MX_DTYPE_F32, x.grad_dtype == MX_DTYPE_F32};
+                        x.lr_mult, flags, 0};
         for (int64_t c = 0; c < ceil_div(x.n, kChunk); ++c) of_chunk[chunks++] = i;
         pos += round_up(x.n, 32);
     }
@@ -504,12 +766,17 @@ int launch_adamw_step(void* plan, const adamw_info& info, int64_t* step, double 
     a.c1 = static_cast<float>(1.0 - beta1);
     a.b2 = static_cast<float>(beta2);
     a.c2 = static_cast<float>(1.0 - beta2);
+    a.root_b2 = static_cast<float>(std::sqrt(beta2));
+    a.root_c2 = static_cast<float>(std::sqrt(1.0 - beta2));
     a.eps = static_cast<float>(eps);
     a.lr_dev = lr_dev;
     a.grad_scale = grad_scale;
     a.seed = seed;
     a.stochastic = stochastic;
-    const unsigned grid = static_cast<unsigned>(info.chunks);
+    const int sms = sm_count();
+    if (sms <= 0) return MX_ERR_CUDA;
+    const int64_t resident = static_cast<int64_t>(sms) * (info.state_bits == 8 ? kStepCtas8 : kStepCtas32);
+    const unsigned grid = static_cast<unsigned>(info.chunks < resident ? info.chunks : resident);
     if (info.state_bits == 8) adamw_step_kernel<true><<<grid, kThreads, 0, stream>>>(plan, a);
     else adamw_step_kernel<false><<<grid, kThreads, 0, stream>>>(plan, a);
     return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
@@ -518,7 +785,7 @@ int launch_adamw_step(void* plan, const adamw_info& info, int64_t* step, double 
 int launch_adamw_norm(void* plan, const adamw_info& info, double max_norm, float* out, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return MX_ERR_CUDA;
-    int64_t grid = static_cast<int64_t>(sms) * 8;
+    int64_t grid = static_cast<int64_t>(sms) * kNormCtasPerSm;   // all resident: equal shares, one wave
     grid = grid > kNormCtas ? kNormCtas : grid;
     grid = grid > info.chunks ? info.chunks : grid;
     adamw_norm_kernel<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(plan, info.tensors, info.chunks,
