@@ -135,6 +135,39 @@ __device__ __forceinline__ Tile get_tile(const Args& g, const int32_t* table, in
     return t;
 }
 
+// Checks that the offsets run from 0 monotonically to at most R (every later address depends on
+// it) and builds the tile list of a pass over rows: table[e] = first tile of expert e, table[E] =
+// tile count, 0 for bad offsets (reported).  LIST = false: the check alone.  One warp calls it; a
+// lane takes a run of experts, its offsets read in one go where there are up to 32 experts a lane.
+template <bool LIST, typename F>
+__device__ __forceinline__ bool build_table(const Args& g, int32_t* table, int lane, bool report, F tiles_of) {
+    const int per = (g.E + 31) / 32, e0 = lane * per;
+    int32_t sum = 0, prev = __ldg(g.off + (e0 < g.E ? e0 : g.E));
+    bool bad = lane == 0 && (prev != 0 || __ldg(g.off + g.E) > g.R);
+    for (int e = e0; e < e0 + per && e < g.E; ++e) {
+        const int32_t next = __ldg(g.off + e + 1);
+        bad |= next < prev;
+        if (LIST) {
+            table[e] = sum;   // within the lane's run
+            sum += next > prev ? tiles_of(static_cast<int64_t>(next) - prev) : 0;
+        }
+        prev = next;
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (LIST) {
+        int32_t incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        for (int e = e0; e < e0 + per && e < g.E; ++e) table[e] += incl - sum;
+        if (lane == 31) table[g.E] = bad ? 0 : incl;
+    }
+    if (bad && report && lane == 0) atomicOr(g.dev_err, MX_DEVERR_BAD_SEGMENTS);
+    return !bad;
+}
+
 // Loads of one K step: this CTA's 128 rows of a and kBRows of b (from row b0 = its first b row).
 // G selects whether the copies complete on a barrier in the pair's leader (2) or in this CTA (1).
 template <int NC, int PASS, int G>
@@ -209,37 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish_g<NC>();
     }
     if (warp == 2) {
-        // Validate the offsets (every later address depends on them) and build the tile list:
-        // table[e] = first tile of expert e, table[E] = tile count.
         const int64_t nt = (g.n_out + BN - 1) / BN;
-        const int per = (g.E + 31) / 32;
-        const int e0 = lane * per;
-        int32_t sum = 0;
-        bool bad = false;
-        for (int e = e0; e < e0 + per && e < g.E; ++e) {
-            const int64_t te = static_cast<int64_t>(__ldg(g.off + e + 1)) - __ldg(g.off + e);
-            bad |= te < 0;
-            if (!kW && te > 0) sum += static_cast<int32_t>((te + C::kTileM - 1) / C::kTileM * nt);
-        }
-        if (lane == 31) bad |= __ldg(g.off) != 0 || __ldg(g.off + g.E) > g.R;
-        bad = __any_sync(0xffffffffu, bad);
-        int32_t incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += v;
-        }
-        if (!kW && !bad) {
-            int32_t run = incl - sum;
-            for (int e = e0; e < e0 + per && e < g.E; ++e) {
-                const int64_t te = static_cast<int64_t>(__ldg(g.off + e + 1)) - __ldg(g.off + e);
-                table[e] = run;
-                run += static_cast<int32_t>((te + C::kTileM - 1) / C::kTileM * nt);
-            }
-        }
-        if (lane == 31) {
-            table[g.E] = bad ? 0 : kW ? static_cast<int32_t>(g.E * ((g.m_out + C::kTileM - 1) / C::kTileM) * nt) : incl;
-            if (bad && leader) atomicOr(g.dev_err, MX_DEVERR_BAD_SEGMENTS);
+        if (kW) {
+            const bool ok = build_table<false>(g, table, lane, leader, [](int64_t) { return 0; });
+            if (lane == 0) table[g.E] = ok ? static_cast<int32_t>(g.E * ((g.m_out + C::kTileM - 1) / C::kTileM) * nt) : 0;
+        } else {
+            build_table<true>(g, table, lane, leader,
+                              [&](int64_t te) { return static_cast<int32_t>((te + C::kTileM - 1) / C::kTileM * nt); });
         }
     }
     tc_fence_before();
@@ -529,6 +538,236 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ------------------------------------------------------------------ few rows per expert
+// Serving and small batches: an expert has a few rows, and the call is bound by reading its
+// weights once.  The operands change places: 128 output columns (weight rows, or columns for
+// dgrad) are the MMA's M side and up to NT of the expert's rows its N side, so no tensor or
+// shared-memory work is spent on rows that do not exist.  Two CTAs share an SM: with one token's
+// eight experts of 4096 x 7168 there are 256 tiles, and every CTA in flight gets an equal share of
+// the bandwidth, so 152 SMs finish 1 or 2 of them together (one CTA an SM with twice the stages:
+// 78 us, two: 74 us, three: 76 us, four: 85 us; the fat tiles: 95 us).  Roles: warp 0 copies, warp
+// 1 MMAs, warp 2 the tile list, warps 4 to 7 the epilogue; two accumulators.
+constexpr int kThinThreads = 256;
+constexpr int kThinCtas = 2;                   // CTAs on an SM
+
+template <int NT>
+struct ThinCfg {
+    static constexpr int kStages = NT == 32 ? 5 : 4;   // of 64 elements each
+    static constexpr uint32_t kWBytes = BM * kRowBytes;            // per K step
+    static constexpr uint32_t kXBytes = NT * kRowBytes;
+    static constexpr uint32_t kOffW = 0;
+    static constexpr uint32_t kOffX = kStages * kWBytes;
+    static constexpr uint32_t kOffBar = kOffX + kStages * kXBytes;
+    static constexpr uint32_t kNumBars = 2 * kStages + 5;
+    static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr uint32_t kOffTable = (kOffMisc + 8 + 15) / 16 * 16;
+    static constexpr uint32_t kSmemBytes = kOffTable + (kMaxE + 1) * 4 + 1024;
+    static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;   // columns: a power of two
+    static_assert(kThinCtas * (kSmemBytes + 1024) <= 233472, "shared memory budget");
+};
+
+struct ThinTile {
+    int e, rows;           // expert, its rows in this tile
+    int64_t row0, n0;      // first row, first output column
+};
+
+template <int NT>
+__device__ __forceinline__ ThinTile thin_tile(const Args& g, const int32_t* table, int64_t L) {
+    int lo = 0, hi = g.E - 1;   // last e with table[e] <= L
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (table[mid] <= L) lo = mid; else hi = mid - 1;
+    }
+    ThinTile t;
+    t.e = lo;
+    const int r0 = __ldg(g.off + lo), te = __ldg(g.off + lo + 1) - r0;
+    const int blocks = (te + NT - 1) / NT;      // row blocks fastest: they share a weight tile
+    const int local = static_cast<int>(L - table[lo]);
+    const int n = local / blocks, b = local - n * blocks;
+    t.n0 = static_cast<int64_t>(n) * BM;
+    t.row0 = static_cast<int64_t>(r0) + b * NT;
+    t.rows = te - b * NT < NT ? te - b * NT : NT;
+    return t;
+}
+
+template <int NT, int PASS>
+__global__ void __launch_bounds__(kThinThreads, kThinCtas)
+    grouped_bf16_thin_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args g) {
+    using C = ThinCfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_full = sbase + C::kOffBar, bar_empty = bar_full + 8 * C::kStages;
+    const uint32_t bar_tmem_full = bar_full + 16 * C::kStages, bar_tmem_empty = bar_tmem_full + 16;
+    const uint32_t bar_drain = bar_tmem_full + 32;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    int32_t* table = reinterpret_cast<int32_t*>(smem + C::kOffTable);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(bar_tmem_full + 8 * a, 1);
+            mbar_init(bar_tmem_empty + 8 * a, 4);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc_g<1>(smem_u32(tmem_slot), C::kTmem);
+        tmem_relinquish_g<1>();
+    }
+    if (warp == 2) {
+        const int nt = static_cast<int>((g.n_out + BM - 1) / BM);
+        build_table<true>(g, table, lane, true, [&](int64_t te) { return static_cast<int32_t>((te + NT - 1) / NT * nt); });
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int64_t total = table[g.E];
+    const int num_kt = static_cast<int>((g.k_len + BK - 1) / BK);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t L = blockIdx.x; L < total && ok; L += gridDim.x) {
+                const ThinTile t = thin_tile<NT>(g, table, L);
+                const int32_t n0 = static_cast<int32_t>(t.n0), r0 = static_cast<int32_t>(t.row0);
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    if (!mbar_wait_bounded(bar_empty + 8 * stage, phase ^ 1u, abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = bar_full + 8 * stage;
+                    const uint32_t w = sbase + C::kOffW + stage * C::kWBytes;
+                    const int32_t k0 = kt * BK;
+                    mbar_arrive_expect_tx(full, C::kWBytes + C::kXBytes);
+                    if constexpr (PASS == kBf16Fwd) {
+                        tma_load_3d_g<1>(w, &tmW, full, k0, n0, t.e);
+                    } else {
+                        tma_load_3d_g<1>(w, &tmW, full, n0, k0, t.e);
+                        tma_load_3d_g<1>(w + 64 * kRowBytes, &tmW, full, n0 + 64, k0, t.e);
+                    }
+                    tma_load_2d_g<1>(sbase + C::kOffX + stage * C::kXBytes, &tmX, full, k0, r0);
+                    ++issued;
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+            }
+            const int64_t outstanding = issued < C::kStages ? issued : C::kStages;   // let them land before exit
+            for (int64_t i = 1; i <= outstanding; ++i) {
+                const int64_t idx = issued - i;
+                mbar_wait_timeout(bar_full + 8 * static_cast<int>(idx % C::kStages),
+                                  static_cast<uint32_t>((idx / C::kStages) & 1), kWaitLimitNs / 4);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, acc_iter = 0;
+            bool ok = true;
+            constexpr bool kMn = PASS == kBf16Dgrad;
+            constexpr uint32_t idesc = idesc_bf16(BM, NT, kMn, false);
+            constexpr uint32_t kLboW = kMn ? 64 * kRowBytes : 16;
+            constexpr uint64_t kStepW = kMn ? 2048 >> 4 : 32 >> 4;
+            for (int64_t L = blockIdx.x; L < total && ok; L += gridDim.x) {
+                const uint32_t acc = acc_iter & 1u;
+                if (!mbar_wait_bounded(bar_tmem_empty + 8 * acc, ((acc_iter >> 1) & 1u) ^ 1u, abort_flag, kWaitLimitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    if (!mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t wd = smem_desc(sbase + C::kOffW + stage * C::kWBytes, kLboW, 1024, 2);
+                    const uint64_t xd = smem_desc(sbase + C::kOffX + stage * C::kXBytes, 16, 1024, 2);
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        mma_bf16_g<1>(tmem_base + acc * NT, wd + k * kStepW, xd + k * (32 >> 4), idesc,
+                                      (kt > 0 || k > 0) ? 1u : 0u);
+                    tc_commit_g<1>(bar_empty + 8 * stage, 1);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc_commit_g<1>(bar_tmem_full + 8 * acc, 1);
+                ++acc_iter;
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+            }
+            tc_commit_g<1>(bar_drain, 1);
+            mbar_wait_timeout(bar_drain, 0, kWaitLimitNs / 4);
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3;
+        uint32_t acc_iter = 0;
+        for (int64_t L = blockIdx.x; L < total; L += gridDim.x) {
+            const ThinTile t = thin_tile<NT>(g, table, L);
+            const uint32_t acc = acc_iter & 1u;
+            uint32_t okw = 1;
+            if (lane == 0) okw = mbar_wait_bounded(bar_tmem_full + 8 * acc, (acc_iter >> 1) & 1u, abort_flag, kWaitLimitNs) ? 1u : 0u;
+            okw = __shfl_sync(0xffffffffu, okw, 0);
+            if (!okw) {
+                if (lane == 0) {
+                    *abort_flag = 1;
+                    atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
+                }
+                break;
+            }
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT;
+            uint32_t r[NT / 32][32];
+#pragma unroll
+            for (int c = 0; c < NT / 32; ++c) tmem_ld_32x32b_x32(taddr + c * 32, r[c]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_tmem_empty + 8 * acc);
+            ++acc_iter;
+            // lane: an output column; register: a row.  A warp writes 64 contiguous bytes of a row.
+            const int64_t n = t.n0 + q * 32 + lane;
+            if (n < g.n_out) {
+                uint16_t* dst = static_cast<uint16_t*>(g.out) + t.row0 * g.n_out + n;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (j < t.rows) dst[j * g.n_out] = static_cast<uint16_t>(pack_bf16x2(__uint_as_float(r[j / 32][j % 32]), 0.f));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_g<1>(tmem_base, C::kTmem);
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (fn == nullptr) {
@@ -602,6 +841,27 @@ int launch_tiles(const Problem& pr, const Args& g, int dev, int num_sms, cudaStr
     return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, g) == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 
+template <int NT, int PASS>
+int launch_thin(const Problem& pr, const Args& g, int dev, int num_sms, cudaStream_t stream) {
+    using C = ThinCfg<NT>;
+    static bool set[64] = {false};
+    auto kern = grouped_bf16_thin_kernel<NT, PASS>;
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmemBytes)) !=
+            cudaSuccess)
+            return MX_ERR_CUDA;
+        set[dev] = true;
+    }
+    CUtensorMap tmW, tmX;
+    const bool ok = (PASS == kBf16Fwd ? make_map(&tmW, pr.B, g.E, pr.N, pr.K, BM, true) : make_map(&tmW, pr.B, g.E, pr.K, pr.N, BK, true)) &&
+                    make_map(&tmX, pr.A, 1, g.R, pr.K, NT, false);
+    if (!ok) return MX_ERR_CUDA;
+    const int64_t tiles = (g.R / NT + (g.E < g.R ? g.E : g.R)) * ceil_div(g.n_out, BM);
+    const unsigned grid = static_cast<unsigned>(tiles < kThinCtas * num_sms ? tiles : kThinCtas * num_sms);
+    kern<<<grid, kThinThreads, C::kSmemBytes, stream>>>(tmW, tmX, g);
+    return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
 }  // namespace
 
 int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32_t* off, int E, int64_t R, int64_t N,
@@ -625,6 +885,18 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
     g.dev_err = dev_err;
     const Problem pr{A, B, N, K};
     const int n = num_sms[dev];
+    // Few rows per expert: the thin tiles, for the forward at up to 32 rows on average, for dgrad
+    // where the fat tiles leave SMs idle.  With 32 experts of 4096 x 7168, thin / fat (us): one
+    // token, 8 experts with a row each: forward 74 / 97, dgrad 73 / 97; 4 rows per expert 272 / 290,
+    // 271 / 262; 32 rows 284 / 296, 268 / 268; 64 rows 322 / 299, 318 / 272.
+    if (!w && R <= 32 * static_cast<int64_t>(E) &&
+        (pass == kBf16Fwd || (E < R ? E : R) * ceil_div(N, BN) < 2 * static_cast<int64_t>(n))) {
+        if (R <= 16 * static_cast<int64_t>(E))
+            return pass == kBf16Fwd ? launch_thin<32, kBf16Fwd>(pr, g, dev, n, stream)
+                                    : launch_thin<32, kBf16Dgrad>(pr, g, dev, n, stream);
+        return pass == kBf16Fwd ? launch_thin<64, kBf16Fwd>(pr, g, dev, n, stream)
+                                : launch_thin<64, kBf16Dgrad>(pr, g, dev, n, stream);
+    }
     const bool pairs = w ? N > BM : R / E >= 512;
     if (pass == kBf16Fwd)
         return pairs ? launch_tiles<2, kBf16Fwd>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Fwd>(pr, g, dev, n, stream);
