@@ -93,44 +93,49 @@ struct Tile {
     int valid_rows;        // of this CTA's 128
 };
 
+// Tile L of the list.  All counts are below 2^31 (checked on the host), so the divisions are 32 bits
+// wide: with 64-bit ones the bookkeeping of a tile took longer than a short group's MMAs.
 template <int NC, bool WGRAD>
-__device__ __forceinline__ Tile get_tile(const Args& g, const int32_t* table, int64_t L, uint32_t rank) {
-    constexpr int TM = Cfg<NC>::kTileM;
+__device__ __forceinline__ Tile get_tile(const Args& g, const int32_t* table, uint32_t L, uint32_t rank) {
+    constexpr uint32_t TM = Cfg<NC>::kTileM;
     Tile t;
-    const int64_t nt = (g.n_out + BN - 1) / BN;
-    int64_t local;
+    const uint32_t nt = (static_cast<uint32_t>(g.n_out) + BN - 1) / BN;
+    uint32_t local;
     if (WGRAD) {
-        const int64_t per_e = ((g.m_out + TM - 1) / TM) * nt;
+        const uint32_t per_e = ((static_cast<uint32_t>(g.m_out) + TM - 1) / TM) * nt;
         t.e = static_cast<int>(L / per_e);
         local = L - t.e * per_e;
     } else {
         int lo = 0, hi = g.E - 1;   // last e with table[e] <= L
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (table[mid] <= L) lo = mid; else hi = mid - 1;
+            if (table[mid] <= static_cast<int32_t>(L)) lo = mid; else hi = mid - 1;
         }
         t.e = lo;
         local = L - table[lo];
     }
-    t.row0 = __ldg(g.off + t.e);
-    const int64_t te = static_cast<int64_t>(__ldg(g.off + t.e + 1)) - t.row0;
+    const int32_t r0 = __ldg(g.off + t.e);
+    const uint32_t te = static_cast<uint32_t>(__ldg(g.off + t.e + 1) - r0);
+    t.row0 = r0;
     // Groups of G M tiles, M fastest inside a group: the CTAs in flight share one b tile, and the
     // group's strip of a (at most 32 MiB) stays in L2 across the N tiles.
-    const int64_t rows = WGRAD ? g.m_out : te;
-    const int64_t kbytes = 2 * (WGRAD ? te : g.k_len);
-    const int64_t mts = (rows + TM - 1) / TM;
-    int64_t G = (int64_t(32) << 20) / (TM * (kbytes > 0 ? kbytes : 1));
-    G = G < 1 ? 1 : (G > mts ? mts : G);
-    const int64_t grp = local / (G * nt);
-    const int64_t in = local - grp * G * nt;
-    const int64_t gs = mts - grp * G < G ? mts - grp * G : G;
-    const int64_t ntile = in / gs;
-    t.m_in = (grp * G + (in - ntile * gs)) * TM + static_cast<int64_t>(rank) * BM;
-    t.n0 = ntile * BN;
-    const int64_t k = WGRAD ? te : g.k_len;
+    const uint32_t rows = WGRAD ? static_cast<uint32_t>(g.m_out) : te;
+    const uint32_t k = WGRAD ? te : static_cast<uint32_t>(g.k_len);
+    const uint32_t mts = (rows + TM - 1) / TM;
+    constexpr uint32_t kStrip = (32u << 20) / (2 * TM);   // G = kStrip / k
+    uint32_t grp = 0, gs = mts, G = mts;
+    if (k * static_cast<uint64_t>(mts) > kStrip) {
+        G = k < kStrip ? kStrip / k : 1;
+        grp = local / (G * nt);
+        local -= grp * G * nt;
+        gs = mts - grp * G < G ? mts - grp * G : G;
+    }
+    const uint32_t ntile = local / gs;
+    t.m_in = static_cast<int64_t>(grp * G + (local - ntile * gs)) * TM + rank * BM;
+    t.n0 = static_cast<int64_t>(ntile) * BN;
     t.num_kt = static_cast<int>((k + BK - 1) / BK);
     t.tail = WGRAD ? static_cast<int>(k % BK) : 0;
-    const int64_t vr = rows - t.m_in;
+    const int64_t vr = static_cast<int64_t>(rows) - t.m_in;
     t.valid_rows = static_cast<int>(vr < 0 ? 0 : (vr < BM ? vr : BM));
     return t;
 }
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t tails = 0;   // bit s: parity of the next tail phase of stage s; bit 8 + s: one was issued
             bool ok = true;
             for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
-                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
                 const int32_t b0 = static_cast<int32_t>(t.n0 + rank * C::kBRows);
                 for (int kt = 0; kt < t.num_kt; kt += C::kSub) {
                     const int nsub = t.num_kt - kt < C::kSub ? t.num_kt - kt : C::kSub;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kLboA = kW ? 64 * kRowBytes : 16, kLboB = PASS != kBf16Fwd ? 64 * kRowBytes : 16;
             constexpr uint64_t kStepA = kW ? 2048 >> 4 : 32 >> 4, kStepB = PASS != kBf16Fwd ? 2048 >> 4 : 32 >> 4;
             for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
-                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
                 for (int kt = 0; kt < t.num_kt && ok; kt += C::kSub) {
                     const uint32_t acc = acc_iter & 1u;
                     const bool first = kW ? kt % kPartSteps == 0 : kt == 0;
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t stages = 0;
             uint32_t tails = 0;   // bit s: parity of stage s's next tail phase
             for (int64_t L = unit; L < total_tiles; L += num_units) {
-                const Tile t = get_tile<NC, kW>(g, table, L, rank);
+                const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
                 stages += (t.num_kt + C::kSub - 1) / C::kSub;
                 if (t.tail == 0) continue;
                 const int stage = static_cast<int>((stages - 1) % C::kStages);
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++acc_iter;
         };
         for (int64_t L = unit; L < total_tiles; L += num_units) {
-            const Tile t = get_tile<NC, kW>(g, table, L, rank);
+            const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
             const bool row_ok = row < t.valid_rows;
             const int64_t col0 = t.n0 + half * 128;
             const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
