@@ -463,20 +463,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t col0 = t.n0 + half * 128;
             const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
             if constexpr (kW) {
-                float sum[128];
+                uint32_t sum[4][32];   // fp32 bits: the first part is loaded as it is, later ones added
+                if (t.num_kt == 0) {   // an expert without rows
 #pragma unroll
-                for (int j = 0; j < 128; ++j) sum[j] = 0.f;
+                    for (int j = 0; j < 128; ++j) sum[j / 32][j % 32] = 0u;
+                }
                 bool ok = true;
                 for (int kt = 0; kt < t.num_kt; kt += kPartSteps) {
                     if (!(ok = acquire())) break;
                     const uint32_t taddr = tmem_base + lanes + (acc_iter & 1u) * BN + half * 128;
+                    if (kt == 0) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
+                        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(taddr + c * 32, sum[c]);
                         tmem_ld_wait();
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld_32x32b_x32(taddr + c * 32, r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                sum[c][j] = __float_as_uint(__uint_as_float(sum[c][j]) + __uint_as_float(r[j]));
+                        }
                     }
                     release();
                 }
@@ -486,14 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         if (col0 + 8 * j < g.n_out) {
-                            const float* s = sum + 8 * j;
+                            const uint32_t* s = sum[j / 4] + 8 * (j % 4);
                             if (g.wide_store) {
-                                st_global_v8(dst + 8 * j, __float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
-                                             __float_as_uint(s[3]), __float_as_uint(s[4]), __float_as_uint(s[5]),
-                                             __float_as_uint(s[6]), __float_as_uint(s[7]), l2_policy_evict_first());
+                                st_global_v8(dst + 8 * j, s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7], l2_policy_evict_first());
                             } else {
-                                reinterpret_cast<float4*>(dst)[2 * j] = make_float4(s[0], s[1], s[2], s[3]);
-                                reinterpret_cast<float4*>(dst)[2 * j + 1] = make_float4(s[4], s[5], s[6], s[7]);
+                                reinterpret_cast<uint4*>(dst)[2 * j] = make_uint4(s[0], s[1], s[2], s[3]);
+                                reinterpret_cast<uint4*>(dst)[2 * j + 1] = make_uint4(s[4], s[5], s[6], s[7]);
                             }
                         }
                     }
