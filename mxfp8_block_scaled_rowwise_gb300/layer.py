@@ -1,6 +1,7 @@
-"""One MXFP8 MoE FFN layer training step (forward + backward) over preallocated device buffers.
+"""One MoE FFN layer training step (forward + backward) over preallocated device buffers, in MXFP8
+(MoEFFNStep) or bf16 (MoEFFNStepBf16), and the AdamW step over its weights (AdamW).
 
-This composes the C-ABI calls of the hot path in the order the pages describe
+The MXFP8 step composes the C-ABI calls of the hot path in the order the pages describe
 (aigc.bar "Blackwell性能陷阱？…MoE提速3.5倍的底层逻辑", section "2. 被忽视的“量化税”":
 quantize the inputs, then the grouped matmuls; backward needs a transpose-quantize
 as well):
@@ -217,3 +218,125 @@ class MoEFFNStep:
             self.gemm_hook = hook
         torch.cuda.current_stream(self.dev).wait_stream(s)
         return graph
+
+
+class MoEFFNStepBf16:
+    """The same layer step with every operand kept in bf16: buffers and launch sequence, with the inputs,
+    outputs and methods of MoEFFNStep (x, ids, gate, dout, w1, w2 in; out, dx, dgate, dw1, dw2 out), for
+    layers that a recipe leaves out of MXFP8.
+
+    forward   routing ids permuted by expert; x gathered into expert order; GEMM1 -> [gate | up]; SwiGLU;
+              GEMM2; combine.
+    backward  combine backward (dY, dgate); dgrad2, wgrad2; SwiGLU backward; dgrad1, wgrad1; un-permute sum.
+
+    No weight is laid out anew per step: the products read w1 [E, 2I, H] and w2 [E, H, I] as they are in
+    both directions.  hidden and inter: multiples of 8."""
+
+    def __init__(self, T: int, E: int, k: int, hidden: int, inter: int, device="cuda"):
+        self.T, self.E, self.k, self.H, self.I = T, E, k, hidden, inter
+        self.I2 = 2 * inter
+        self.R = R = T * k
+        dev = torch.device(device)
+        self.dev = dev
+        H, I, I2 = hidden, inter, 2 * inter
+        bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+
+        def z(*shape, dtype=bf):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        # inputs (filled by the caller)
+        self.x, self.dout = z(T, H), z(T, H)
+        self.ids, self.gate = z(T, k, dtype=i32), z(T, k, dtype=f32)
+        self.w1, self.w2 = z(E, I2, H), z(E, H, I)
+        # routing
+        self.counts, self.off, self.poff = z(E, dtype=i32), z(E + 1, dtype=i32), z(E + 1, dtype=i32)
+        self.src_row, self.dst_of = z(R, dtype=i32), z(R, dtype=i32)
+        self.ws_bytes = mx.moe_permute_workspace_bytes(T, k, E)
+        self.ws = z(max(self.ws_bytes, 16), dtype=torch.uint8)
+        # activations and gradients in expert order
+        self.xp, self.out1, self.h, self.out2 = z(R, H), z(R, I2), z(R, I), z(R, H)
+        self.dy, self.dh_in, self.da, self.dx_routed = z(R, H), z(R, I), z(R, I2), z(R, H)
+        self.out, self.dx, self.dgate = z(T, H), z(T, H), z(T, k, dtype=f32)
+        self.dw1, self.dw2 = z(E, I2, H, dtype=f32), z(E, H, I, dtype=f32)
+        self.dev_err = torch.zeros(1, dtype=i32, device=dev)
+        self.gemm_hook = None      # optional callable(name, flops, fn) wrapping each GEMM launch
+        self.launches = 0          # CUDA kernels launched by this object
+
+    gemm_flops = MoEFFNStep.gemm_flops
+    _gemm = MoEFFNStep._gemm
+    step = MoEFFNStep.step
+    capture = MoEFFNStep.capture
+
+    def forward(self):
+        T, E, k, H, I, I2, R = self.T, self.E, self.k, self.H, self.I, self.I2, self.R
+        self.launches += 6
+        mx.moe_permute(self.ids, T, k, E, self.counts, self.off, self.poff, self.src_row, self.dst_of,
+                       None, None, 0, None, None, self.ws, self.ws_bytes, self.dev_err)
+        mx.moe_gather_rows(self.x, 2 * H, self.src_row, R, self.xp)
+        self._gemm("fwd1", lambda: mx.grouped_gemm_bf16_fwd(self.xp, self.w1, self.off, E, R, I2, H, self.out1,
+                                                            self.dev_err))
+        mx.moe_swiglu_fwd(self.out1, R, I, self.h)
+        self._gemm("fwd2", lambda: mx.grouped_gemm_bf16_fwd(self.h, self.w2, self.off, E, R, H, I, self.out2,
+                                                            self.dev_err))
+        mx.moe_combine_fwd(self.out2, self.gate, self.dst_of, T, k, H, R, self.out, self.dev_err)
+
+    def backward(self):
+        T, E, k, H, I, I2, R = self.T, self.E, self.k, self.H, self.I, self.I2, self.R
+        self.launches += 3
+        mx.moe_combine_bwd(self.dout, self.out2, self.gate, self.dst_of, T, k, H, R, self.dy, self.dgate, self.dev_err)
+        self._gemm("dgrad2", lambda: mx.grouped_gemm_bf16_dgrad(self.dy, self.w2, self.off, E, R, I, H, self.dh_in,
+                                                                self.dev_err))
+        self._gemm("wgrad2", lambda: mx.grouped_gemm_bf16_wgrad(self.dy, self.h, self.off, E, R, H, I, self.dw2,
+                                                                self.dev_err))
+        mx.moe_swiglu_bwd(self.dh_in, self.out1, R, I, self.da)
+        self._gemm("dgrad1", lambda: mx.grouped_gemm_bf16_dgrad(self.da, self.w1, self.off, E, R, H, I2, self.dx_routed,
+                                                                self.dev_err))
+        self._gemm("wgrad1", lambda: mx.grouped_gemm_bf16_wgrad(self.da, self.xp, self.off, E, R, I2, H, self.dw1,
+                                                                self.dev_err))
+        mx.moe_combine_fwd(self.dx_routed, None, self.dst_of, T, k, H, R, self.dx, self.dev_err)
+
+
+class AdamW:
+    """AdamW over lists of tensors: their moments (fp32, or 8 bits with block scales), plan, step count and
+    clipping factor, all on the device, so that a step can be part of a CUDA graph.
+
+    params / grads: contiguous CUDA tensors, bf16 or fp32; e.g. [layer.w1, layer.w2] and [layer.dw1,
+    layer.dw2].  copies: bf16 copies of fp32 params, written with them (None entries allowed).
+    max_norm > 0 clips the norm of all gradients to it, and skips a step whose gradients are not finite.
+    stochastic: bf16 params are rounded stochastically, which keeps updates below half a unit in their last
+    place from being lost."""
+
+    def __init__(self, params, grads, state_bits: int = 32, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, lr_mult=1.0, max_norm: float = 0.0, stochastic: bool = False, seed: int = 0,
+                 copies=None):
+        if state_bits not in (8, 32):
+            raise mx.MxError("AdamW: state_bits is 8 or 32, not %r" % (state_bits,))
+        dev = params[0].device
+        dtype = torch.uint8 if state_bits == 8 else torch.float32
+
+        def zeros(n, t):
+            return torch.zeros(n, dtype=t, device=dev)
+        self.moments = [zeros(p.numel(), dtype) for p in params]
+        self.seconds = [zeros(p.numel(), dtype) for p in params]
+        blocks = [(p.numel() + 31) // 32 for p in params]
+        self.scale_m = [zeros(n, torch.uint8) for n in blocks] if state_bits == 8 else None
+        self.scale_r = [zeros(n, torch.uint8) for n in blocks] if state_bits == 8 else None
+        self.plan = mx.adamw_plan(params, grads, self.moments, self.seconds, self.scale_m, self.scale_r, copies,
+                                  weight_decay, lr_mult)
+        self.steps = torch.zeros(1, dtype=torch.int64, device=dev)   # steps taken
+        self.lr = torch.full((1,), lr, dtype=torch.float32, device=dev)
+        self.norm = torch.zeros(2, dtype=torch.float32, device=dev)  # gradient norm, clipping factor
+        self._scale = self.norm[1:]
+        self.betas, self.eps, self.max_norm, self.stochastic, self.seed = betas, eps, max_norm, stochastic, seed
+
+    def set_lr(self, lr: float):
+        """The learning rate of the steps from here on, replays of a captured step among them."""
+        self.lr.fill_(lr)
+
+    def step(self):
+        scale = None
+        if self.max_norm > 0:
+            mx.adamw_grad_norm(self.plan, self.max_norm, self.norm)
+            scale = self._scale
+        mx.adamw_step(self.plan, self.steps, 0.0, self.betas[0], self.betas[1], self.eps, self.lr, scale, self.seed,
+                      self.stochastic)
