@@ -155,7 +155,7 @@ def _stream(stream=None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None and torch.cuda.is_initialized():
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -355,6 +355,7 @@ class AdamwPlan:
 
     def __init__(self, device_image, info, tensors, starts):
         self.image, self.info, self.tensors, self.starts = device_image, info, tensors, starts
+        self._image, self._info = device_image.data_ptr(), ctypes.byref(info)
 
     @property
     def positions(self) -> int:
@@ -424,16 +425,17 @@ def adamw_grad_norm(plan: AdamwPlan, max_norm: float, out, stream=None):
     """out (fp32 [2]) = norm of all gradients, and the factor that clips it to max_norm (0: no clipping)."""
     if out.dtype != torch.float32 or out.numel() < 2:
         raise MxError("adamw_grad_norm: out is fp32 [2]")
-    st = load().adamw_grad_norm(_ptr(plan.image), ctypes.byref(plan.info), max_norm, _ptr(out), _stream(stream))
+    st = load().adamw_grad_norm(plan._image, plan._info, max_norm, _ptr(out), _stream(stream))
     _check(st, "adamw_grad_norm")
 
 
 def adamw_step(plan: AdamwPlan, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, lr_dev=None, grad_scale=None, seed=0,
                stochastic=False, stream=None):
     """One AdamW step over the plan's tensors; step: int64 [1] on the device, the steps taken so far."""
-    if step.dtype != torch.int64 or any(t is not None and t.dtype != torch.float32 for t in (lr_dev, grad_scale)):
+    if (step.dtype is not torch.int64 or (lr_dev is not None and lr_dev.dtype is not torch.float32) or
+            (grad_scale is not None and grad_scale.dtype is not torch.float32)):
         raise MxError("adamw_step: step is int64 [1], lr_dev and grad_scale are fp32 [1]")
-    st = load().adamw_step(_ptr(plan.image), ctypes.byref(plan.info), _ptr(step), lr, beta1, beta2, eps, _ptr(lr_dev),
+    st = load().adamw_step(plan._image, plan._info, _ptr(step), lr, beta1, beta2, eps, _ptr(lr_dev),
                            _ptr(grad_scale), seed & 0xFFFFFFFF, MX_ADAMW_STOCHASTIC if stochastic else 0,
                            _stream(stream))
     _check(st, "adamw_step")
@@ -443,8 +445,7 @@ def adamw_state_values(plan: AdamwPlan, moment, root, stream=None):
     """The values of 8-bit moments as bf16 [plan.positions] each: m, and r = sqrt(v)."""
     if any(t.dtype != torch.bfloat16 or t.numel() < plan.positions for t in (moment, root)):
         raise MxError("adamw_state_values: moment and root are bf16 [plan.positions]")
-    st = load().adamw_state_values(_ptr(plan.image), ctypes.byref(plan.info), _ptr(moment), _ptr(root),
-                                   _stream(stream))
+    st = load().adamw_state_values(plan._image, plan._info, _ptr(moment), _ptr(root), _stream(stream))
     _check(st, "adamw_state_values")
 
 

@@ -536,69 +536,185 @@ __device__ __forceinline__ void step32(const Slot& sl, int64_t at, int valid, co
     if (sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
 }
 
-template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads, EIGHT ? kStepCtas8 : kStepCtas32) adamw_step_kernel(void* plan, const StepArgs a) {
-    const PlanView pv = view(plan, a.n);
+// What all elements of a step share.
+struct StepShared {
+    float gs, lr, inv_bc1, inv_v;
+    int64_t t;
+    uint32_t key0;
+};
+
+// false: the gradients were not finite, the step is skipped and t stays
+__device__ __forceinline__ bool begin_step(const StepArgs& a, StepShared& s) {
     __shared__ float s_bc[2];
-    const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-    const int64_t t = *a.step + 1;
-    if (!isfinite(gs)) return;   // the gradients were not finite: the step is skipped, t stays
+    s.gs = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
+    s.t = *a.step + 1;
+    if (!isfinite(s.gs)) return false;
     if (threadIdx.x == 0) {
-        s_bc[0] = 1.0f / -expm1f(static_cast<float>(static_cast<double>(t) * a.log_b1));     // 1 / (1 - b1^t)
-        s_bc[1] = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(t) * a.log_b2)));   // (1 - b2^t)^-1/2
+        s_bc[0] = 1.0f / -expm1f(static_cast<float>(static_cast<double>(s.t) * a.log_b1));     // 1 / (1 - b1^t)
+        s_bc[1] = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(s.t) * a.log_b2)));   // (1 - b2^t)^-1/2
     }
     __syncthreads();
-    const float lr0 = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
-    const float inv_bc1 = s_bc[0];
-    Rate k;
-    k.inv_v = s_bc[1];
-    k.eps = a.eps;
-    const uint32_t key0 = step_key(a.seed, t);
+    s.inv_bc1 = s_bc[0];
+    s.inv_v = s_bc[1];
+    s.lr = a.lr_dev != nullptr ? *a.lr_dev : a.lr;
+    s.key0 = step_key(a.seed, s.t);
+    return true;
+}
+
+// Every CTA has read the step by now: the last to arrive here counts it.
+__device__ __forceinline__ void end_step(const PlanView& pv, const StepArgs& a, const StepShared& s) {
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(&pv.h->step_done, 1u) == gridDim.x - 1) {
+            pv.h->step_done = 0;
+            *a.step = s.t;
+        }
+    }
+}
+
+// Asynchronous copies of a thread's own 8 gradients and codes into its own places of a stage, so that
+// no thread waits for another.  A stage is 32 + 8 + 8 bytes a thread; the two halves of 8 fp32
+// gradients change places in every second group of four threads, which keeps 16-byte reads of 8
+// neighbours on 32 different banks.
+constexpr int kStages = 3, kStageBytes = kThreads * 48;
+static_assert(kStages * kStageBytes <= 48 * 1024, "within the default dynamic shared memory");
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void stage_in(const Slot& sl, int64_t at, uint32_t stage, uint32_t tid) {
+    const uint32_t g = stage + tid * 32, flip = (tid >> 2 & 1) * 16;
+    if (sl.flags & kGradF32) {
+        const float* src = static_cast<const float*>(sl.g) + at;
+        cp_async_16(g + flip, src);
+        cp_async_16(g + (flip ^ 16), src + 4);
+    } else {
+        cp_async_16(g + flip, static_cast<const uint16_t*>(sl.g) + at);
+    }
+    cp_async_8(stage + kThreads * 32 + tid * 8, static_cast<const uint8_t*>(sl.m) + at);
+    cp_async_8(stage + kThreads * 40 + tid * 8, static_cast<const uint8_t*>(sl.v) + at);
+}
+
+__device__ __forceinline__ uint4 lds_16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void stage_out(const Slot& sl, uint32_t stage, uint32_t tid, Raw8& x) {
+    const uint32_t g = stage + tid * 32, flip = (tid >> 2 & 1) * 16;
+    const uint4 a = lds_16(g + flip);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if (sl.flags & kGradF32) {
+        const uint4 b = lds_16(g + (flip ^ 16));
+        x.g[0] = __uint_as_float(a.x); x.g[1] = __uint_as_float(a.y); x.g[2] = __uint_as_float(a.z); x.g[3] = __uint_as_float(a.w);
+        x.g[4] = __uint_as_float(b.x); x.g[5] = __uint_as_float(b.y); x.g[6] = __uint_as_float(b.z); x.g[7] = __uint_as_float(b.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.g[2 * i] = bf16_lo(w[i]);
+            x.g[2 * i + 1] = bf16_hi(w[i]);
+        }
+    }
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.m[0]), "=r"(x.m[1]) : "r"(stage + kThreads * 32 + tid * 8) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.r[0]), "=r"(x.r[1]) : "r"(stage + kThreads * 40 + tid * 8) : "memory");
+}
+
+// One CTA's run of consecutive chunks, tensor by tensor.  Within a tensor the groups of 2048
+// elements are a pipeline: gradients and codes two groups ahead in shared memory, scale bytes one
+// group ahead in registers, the parameters (needed last) at the start of their own.  A tensor's
+// last, partly filled group is loaded directly.
+__global__ void __launch_bounds__(kThreads, kStepCtas8) adamw_step8_kernel(void* plan, const StepArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    StepShared sh;
+    if (!begin_step(a, sh)) return;
+    const PlanView pv = view(plan, a.n);
+    const uint32_t tid = threadIdx.x;
+    const uint32_t base = smem_u32(smem);
+    const int64_t c0 = a.chunks * blockIdx.x / gridDim.x, c1 = a.chunks * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t chunk = c0; chunk < c1;) {
+        const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
+        const int64_t chunks_here = (sl.n + kChunk - 1) / kChunk;
+        const int64_t last = sl.chunk0 + chunks_here < c1 ? sl.chunk0 + chunks_here : c1;
+        const int64_t e0 = (chunk - sl.chunk0) * kChunk;                                   // elements [e0, e1)
+        const int64_t e1 = sl.n < (last - sl.chunk0) * kChunk ? sl.n : (last - sl.chunk0) * kChunk;
+        chunk = last;
+        Rate k;
+        const float lr = sh.lr * sl.lr_mult;
+        k.keep = 1.0f - lr * sl.wd;
+        k.neg_lr_t = -lr * sh.inv_bc1;
+        k.inv_v = sh.inv_v;
+        k.eps = a.eps;
+        const int64_t full = (e1 - e0) / kGroup;
+        int64_t at = e0 + tid * kPer;
+        for (int i = 0; i < 2; ++i) {
+            if (i < full) stage_in(sl, at + i * kGroup, base + i * kStageBytes, tid);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        uint32_t sm = 0, sr = 0;
+        if (full > 0) {
+            sm = sl.sm[at / 32];
+            sr = sl.sr[at / 32];
+        }
+        uint32_t cur = 0;
+        for (int64_t i = 0; i < full; ++i, at += kGroup) {
+            Raw8 x;
+            x.sm = sm;
+            x.sr = sr;
+            load_any(sl.p, (sl.flags & kParamF32) != 0, at, kPer, (sl.flags & kWide) != 0, x.p);
+            if (i + 1 < full) {
+                sm = sl.sm[(at + kGroup) / 32];
+                sr = sl.sr[(at + kGroup) / 32];
+            }
+            // the stage filled now was read one group ago
+            const uint32_t into = cur == 0 ? 2 : cur - 1;
+            if (i + 2 < full) stage_in(sl, at + 2 * kGroup, base + into * kStageBytes, tid);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            stage_out(sl, base + cur * kStageBytes, tid, x);
+            cur = cur == 2 ? 0 : cur + 1;
+            const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
+            step8(sl, at, kPer, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
+        }
+        if (e0 + full * kGroup < e1) {   // the tensor's end
+            Raw8 x;
+            const int valid = valid_of(sl.n, at);
+            load8(sl, at, valid, x);
+            const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
+            step8(sl, at, valid, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    end_step(pv, a, sh);
+}
+
+__global__ void __launch_bounds__(kThreads, kStepCtas32) adamw_step32_kernel(void* plan, const StepArgs a) {
+    StepShared sh;
+    if (!begin_step(a, sh)) return;
+    const PlanView pv = view(plan, a.n);
     // a run of consecutive chunks for every CTA, so that the tensor rarely changes
     const int64_t c0 = a.chunks * blockIdx.x / gridDim.x, c1 = a.chunks * (blockIdx.x + 1) / gridDim.x;
     for (int64_t chunk = c0; chunk < c1; ++chunk) {
         const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
         const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
-        const int v0 = valid_of(sl.n, at), v1 = valid_of(sl.n, at + kGroup);
-        // the tensor's next chunk on its way into L2 during this one's arithmetic
-        if (EIGHT && threadIdx.x < 4 && chunk + 1 < c1) {
-            const int64_t nx = (chunk + 1 - sl.chunk0) * kChunk;
-            int64_t cnt = sl.n - nx;
-            cnt = cnt > kChunk ? kChunk : cnt;
-            const int sh = threadIdx.x == 0 ? ((sl.flags & kGradF32) ? 2 : 1) : threadIdx.x == 1 ? ((sl.flags & kParamF32) ? 2 : 1) : 0;
-            const char* base = static_cast<const char*>(threadIdx.x == 0 ? sl.g : threadIdx.x == 1 ? sl.p : threadIdx.x == 2 ? sl.m : sl.v);
-            const int64_t bytes = cnt * (1 << sh) & ~int64_t(15);
-            if (bytes > 0)
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(base + nx * (1 << sh)), "r"(static_cast<uint32_t>(bytes)));
-        }
-        const float lr = lr0 * sl.lr_mult;
+        Rate k;
+        const float lr = sh.lr * sl.lr_mult;
         k.keep = 1.0f - lr * sl.wd;
-        k.neg_lr_t = -lr * inv_bc1;
-        const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
-        const uint32_t key = mix(key0 + static_cast<uint32_t>(pos >> 32));
-        const uint64_t pos1 = pos + kGroup;
-        const uint32_t key1 = mix(key0 + static_cast<uint32_t>(pos1 >> 32));
-        if (EIGHT) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                Raw8 x;
-                const int vv = h ? v1 : v0;
-                load8(sl, at + h * kGroup, vv, x);
-                step8(sl, at + h * kGroup, vv, x, a, gs, k, static_cast<uint32_t>(h ? pos1 : pos), h ? key1 : key);
-            }
-        } else {
-            step32(sl, at, v0, a, gs, k, static_cast<uint32_t>(pos), key);
-            step32(sl, at + kGroup, v1, a, gs, k, static_cast<uint32_t>(pos1), key1);
+        k.neg_lr_t = -lr * sh.inv_bc1;
+        k.inv_v = sh.inv_v;
+        k.eps = a.eps;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at + h * kGroup);
+            step32(sl, at + h * kGroup, valid_of(sl.n, at + h * kGroup), a, sh.gs, k, static_cast<uint32_t>(pos),
+                   mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
         }
     }
-    // every CTA has read the step by now: the last to arrive here counts it
-    if (threadIdx.x == 0) {
-        __threadfence();
-        if (atomicAdd(&pv.h->step_done, 1u) == gridDim.x - 1) {
-            pv.h->step_done = 0;
-            *a.step = t;
-        }
-    }
+    end_step(pv, a, sh);
 }
 
 // ------------------------------------------------------------------ the gradient norm
@@ -777,8 +893,11 @@ int launch_adamw_step(void* plan, const adamw_info& info, int64_t* step, double 
     if (sms <= 0) return MX_ERR_CUDA;
     const int64_t resident = static_cast<int64_t>(sms) * (info.state_bits == 8 ? kStepCtas8 : kStepCtas32);
     const unsigned grid = static_cast<unsigned>(info.chunks < resident ? info.chunks : resident);
-    if (info.state_bits == 8) adamw_step_kernel<true><<<grid, kThreads, 0, stream>>>(plan, a);
-    else adamw_step_kernel<false><<<grid, kThreads, 0, stream>>>(plan, a);
+    if (info.state_bits == 8) {
+        adamw_step8_kernel<<<grid, kThreads, kStages * kStageBytes, stream>>>(plan, a);
+    } else {
+        adamw_step32_kernel<<<grid, kThreads, 0, stream>>>(plan, a);
+    }
     return cudaGetLastError() == cudaSuccess ? MX_OK : MX_ERR_CUDA;
 }
 
