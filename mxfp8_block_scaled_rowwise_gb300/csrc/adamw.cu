@@ -32,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 8;                        // consecutive elements of a thread
 constexpr int kGroup = kThreads * kPer;        // elements that a CTA takes in one go
 constexpr int kChunk = 2 * kGroup;             // elements of a chunk: what a CTA does for one look at the plan
-constexpr int kStepCtas32 = 4, kStepCtas8 = 4; // CTAs of the step on an SM (64 and 80 registers a thread)
+constexpr int kStepCtas32 = 4, kStepCtas8 = 4; // CTAs of the step on an SM (64 registers a thread)
 constexpr int kNormCtasPerSm = 5;
 constexpr int kNormCtas = 1024;                // most CTAs of the norm
 
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas32) adamw_step32_kernel(voi
 }
 
 // ------------------------------------------------------------------ the gradient norm
-// Squares are summed in fp32 over a thread's 16 elements of 2 chunks and in 64 bits above that, in
+// Squares are summed in fp32 over 32 elements of a thread and in 64 bits above that, in
 // a fixed order: per thread over its chunks, per warp and CTA by a tree, over the CTAs in order.
 __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) adamw_norm_kernel(void* plan, int n, int64_t chunks, float max_norm,
                                                               float* out) {
@@ -727,24 +727,35 @@ __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) adamw_norm_kernel(vo
     __shared__ bool s_last;
     double sum = 0.0;
     const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t chunk = c0; chunk < c1; chunk += 2) {
-        float g[4][kPer];   // two groups each of two chunks
+    for (int64_t chunk = c0; chunk < c1;) {   // tensor by tensor
+        const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
+        const int64_t end = sl.chunk0 + (sl.n + kChunk - 1) / kChunk;
+        const int64_t last = end < c1 ? end : c1;
+        const int64_t e0 = (chunk - sl.chunk0) * kChunk;
+        const int64_t e1 = sl.n < (last - sl.chunk0) * kChunk ? sl.n : (last - sl.chunk0) * kChunk;
+        chunk = last;
+        const bool f32 = (sl.flags & kGradF32) != 0, wide = (sl.flags & kWide) != 0;
+        int64_t at = e0 + threadIdx.x * kPer;
+        float part[4];
+        auto square = [](const float (&g)[kPer]) {
+            float x = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool in = chunk + k / 2 < c1;
-            const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + (in ? chunk + k / 2 : chunk)));
-            const int64_t at = (chunk + k / 2 - sl.chunk0) * kChunk + (k & 1) * kGroup + threadIdx.x * kPer;
-            load_any(sl.g, (sl.flags & kGradF32) != 0, at, in ? valid_of(sl.n, at) : 0, (sl.flags & kWide) != 0, g[k]);
+            for (int i = 0; i < kPer; ++i) x = fmaf(g[i], g[i], x);
+            return x;
+        };
+        for (int64_t left = (e1 - e0) / (4 * kGroup); left > 0; --left, at += 4 * kGroup) {
+            float g[4][kPer];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load_any(sl.g, f32, at + k * kGroup, kPer, wide, g[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[k] = square(g[k]);
+            sum += static_cast<double>((part[0] + part[1]) + (part[2] + part[3]));
         }
-        float part = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) s = fmaf(g[k][i], g[k][i], s);
-            part += s;
+        for (; at - threadIdx.x * kPer < e1; at += kGroup) {   // what is left of the tensor: under four groups
+            float g[kPer];
+            load_any(sl.g, f32, at, valid_of(e1, at), wide, g);
+            sum += static_cast<double>(square(g));
         }
-        sum += static_cast<double>(part);
     }
     auto block_sum = [&](double x) {
 #pragma unroll

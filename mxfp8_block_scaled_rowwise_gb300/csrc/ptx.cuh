@@ -427,19 +427,6 @@ __device__ __forceinline__ void tma_load_3d_g(uint32_t dst, const CUtensorMap* m
     }
 }
 
-// Box of shared memory to global memory, as one bulk group of the issuing thread; parts of the box
-// outside the tensor are not written.
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t c0, int32_t c1, int32_t c2) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
-                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(src)
-                 : "memory");
-}
-// The issuing thread's stores have read their shared memory / are complete.
-template <int N>   // all but the last N
-__device__ __forceinline__ void bulk_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // Ordinary shared-memory writes of this thread made visible to the asynchronous proxy (TMA, MMA).
 __device__ __forceinline__ void fence_proxy_async() {
     asm volatile("fence.proxy.async;" ::: "memory");
