@@ -909,7 +909,11 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
         return pass == kBf16Fwd ? launch_thin<64, kBf16Fwd>(pr, g, dev, n, stream)
                                 : launch_thin<64, kBf16Dgrad>(pr, g, dev, n, stream);
     }
-    const bool pairs = w ? N > BM : R / E >= 512;
+    // CTA pairs for long groups, single CTAs (finer tiles, no cluster to start) for short ones.  Single /
+    // pairs (us), 32 experts of 4096 x 7168: forward at 128 rows per expert 310 / 326, 256 rows 467 /
+    // 440, 1024 rows 1286 / 1224; 128 experts of very uneven popularity, 256 rows on average 372 / 400.
+    // Weight gradient of 7168 x 2048 at 16 rows 418 / 443, 128 rows 440 / 448; of 128 columns 20 / 29.
+    const bool pairs = w ? N > BM && R > 128 * static_cast<int64_t>(E) : R >= 512 * static_cast<int64_t>(E);
     if (pass == kBf16Fwd)
         return pairs ? launch_tiles<2, kBf16Fwd>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Fwd>(pr, g, dev, n, stream);
     if (pass == kBf16Dgrad)
