@@ -408,6 +408,10 @@ __device__ __forceinline__ float updated(float p, float m, float r, const Rate& 
     return fmaf(p, k.keep, k.neg_lr_t * m * rcp_approx_ftz(fmaf(r, k.inv_v, k.eps)));
 }
 
+// Kinds of parameter: what a tensor's loop is compiled for (with the test of them in the loop, 22
+// branches a thread and group).
+constexpr int kBf16Nearest = 0, kBf16Stochastic = 1, kF32 = 2;
+
 // What one thread brings of 8 elements.
 struct Raw8 {
     float p[kPer], g[kPer];
@@ -419,6 +423,7 @@ __device__ __forceinline__ int valid_of(int64_t n, int64_t at) {
     return left >= kPer ? kPer : (left > 0 ? static_cast<int>(left) : 0);
 }
 
+template <int P, bool GF32>
 __device__ __forceinline__ void load8(const Slot& sl, int64_t at, int valid, Raw8& x) {
     load_bytes(static_cast<const uint8_t*>(sl.m) + at, valid, x.m);
     load_bytes(static_cast<const uint8_t*>(sl.v) + at, valid, x.r);
@@ -427,8 +432,8 @@ __device__ __forceinline__ void load8(const Slot& sl, int64_t at, int valid, Raw
         asm("ld.global.u8 %0, [%1];" : "=r"(x.sm) : "l"(sl.sm + at / 32));
         asm("ld.global.u8 %0, [%1];" : "=r"(x.sr) : "l"(sl.sr + at / 32));
     }
-    load_any(sl.g, (sl.flags & kGradF32) != 0, at, valid, (sl.flags & kWide) != 0, x.g);
-    load_any(sl.p, (sl.flags & kParamF32) != 0, at, valid, (sl.flags & kWide) != 0, x.p);
+    load_any(sl.g, GF32, at, valid, (sl.flags & kWide) != 0, x.g);
+    load_any(sl.p, P == kF32, at, valid, (sl.flags & kWide) != 0, x.p);
 }
 
 // The step on 8 elements with 8-bit moments.  Scales and factors fold into one:
@@ -438,10 +443,10 @@ __device__ __forceinline__ void load8(const Slot& sl, int64_t at, int valid, Raw
 // gradient; any other warp takes the long ones.  Bound by instructions: 119 a thread's element
 // with IEEE square root and quotient and branches per element, 83 without them, about 50 with
 // packed arithmetic and the short codes.
+template <int P>
 __device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw8& x, const StepArgs& a, float gs,
                                       const Rate& k, uint32_t pos_lo, uint32_t key) {
-    const bool p_f32 = (sl.flags & kParamF32) != 0;
-    const bool sr_p = a.stochastic && !p_f32;
+    constexpr bool p_f32 = P == kF32, sr_p = P == kBf16Stochastic;
     uint32_t u[kPer], wp[4], wm[2], wr[2];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) u[i] = mix((pos_lo ^ key) ^ i);   // (pos_lo is a multiple of 8)
@@ -501,7 +506,7 @@ __device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw
     if (!sr_p) nearest_params(x.p, wp);
     if (p_f32) store_f32(static_cast<float*>(sl.p) + at, valid, (sl.flags & kWide) != 0, x.p);
     else store_words(static_cast<uint16_t*>(sl.p) + at, valid, wp);
-    if (sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
+    if (p_f32 && sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
 }
 
 // The step on 8 elements with fp32 moments.  Bound by HBM: 24 to 30 bytes an element.
@@ -586,9 +591,10 @@ __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
+template <bool GF32>
 __device__ __forceinline__ void stage_in(const Slot& sl, int64_t at, uint32_t stage, uint32_t tid) {
     const uint32_t g = stage + tid * 32, flip = (tid >> 2 & 1) * 16;
-    if (sl.flags & kGradF32) {
+    if constexpr (GF32) {
         const float* src = static_cast<const float*>(sl.g) + at;
         cp_async_16(g + flip, src);
         cp_async_16(g + (flip ^ 16), src + 4);
@@ -605,11 +611,12 @@ __device__ __forceinline__ uint4 lds_16(uint32_t p) {
     return v;
 }
 
-__device__ __forceinline__ void stage_out(const Slot& sl, uint32_t stage, uint32_t tid, Raw8& x) {
+template <bool GF32>
+__device__ __forceinline__ void stage_out(uint32_t stage, uint32_t tid, Raw8& x) {
     const uint32_t g = stage + tid * 32, flip = (tid >> 2 & 1) * 16;
     const uint4 a = lds_16(g + flip);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    if (sl.flags & kGradF32) {
+    if constexpr (GF32) {
         const uint4 b = lds_16(g + (flip ^ 16));
         x.g[0] = __uint_as_float(a.x); x.g[1] = __uint_as_float(a.y); x.g[2] = __uint_as_float(a.z); x.g[3] = __uint_as_float(a.w);
         x.g[4] = __uint_as_float(b.x); x.g[5] = __uint_as_float(b.y); x.g[6] = __uint_as_float(b.z); x.g[7] = __uint_as_float(b.w);
@@ -624,23 +631,67 @@ __device__ __forceinline__ void stage_out(const Slot& sl, uint32_t stage, uint32
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.r[0]), "=r"(x.r[1]) : "r"(stage + kThreads * 40 + tid * 8) : "memory");
 }
 
-// One CTA's run of consecutive chunks, tensor by tensor.  Within a tensor the groups of 2048
-// elements are a pipeline: gradients and codes two groups ahead in shared memory, scale bytes one
-// group ahead in registers, the parameters (needed last) at the start of their own.  A tensor's
-// last, partly filled group is loaded directly.
+// Elements [e0, e1) of a tensor: the groups of 2048 are a pipeline, gradients and codes two groups
+// ahead in shared memory, scale bytes one group ahead in registers, the parameters (needed last) at
+// the start of their own.  A tensor's last, partly filled group is loaded directly.
+template <int P, bool GF32>
+__device__ __forceinline__ void run8(const Slot& sl, int64_t e0, int64_t e1, const StepArgs& a, const StepShared& sh,
+                                     const Rate& k, uint32_t base) {
+    const uint32_t tid = threadIdx.x;
+    const int64_t full = (e1 - e0) / kGroup;
+    int64_t at = e0 + tid * kPer;
+    for (int i = 0; i < 2; ++i) {
+        if (i < full) stage_in<GF32>(sl, at + i * kGroup, base + i * kStageBytes, tid);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    uint32_t sm = 0, sr = 0;
+    if (full > 0) {
+        sm = sl.sm[at / 32];
+        sr = sl.sr[at / 32];
+    }
+    uint32_t cur = 0;
+    for (int64_t i = 0; i < full; ++i, at += kGroup) {
+        Raw8 x;
+        x.sm = sm;
+        x.sr = sr;
+        load_any(sl.p, P == kF32, at, kPer, (sl.flags & kWide) != 0, x.p);
+        if (i + 1 < full) {
+            sm = sl.sm[(at + kGroup) / 32];
+            sr = sl.sr[(at + kGroup) / 32];
+        }
+        // the stage filled now was read one group ago
+        const uint32_t into = cur == 0 ? 2 : cur - 1;
+        if (i + 2 < full) stage_in<GF32>(sl, at + 2 * kGroup, base + into * kStageBytes, tid);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        stage_out<GF32>(base + cur * kStageBytes, tid, x);
+        cur = cur == 2 ? 0 : cur + 1;
+        const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
+        step8<P>(sl, at, kPer, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
+    }
+    if (e0 + full * kGroup < e1) {   // the tensor's end
+        Raw8 x;
+        const int valid = valid_of(sl.n, at);
+        load8<P, GF32>(sl, at, valid, x);
+        const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
+        step8<P>(sl, at, valid, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// One CTA's run of consecutive chunks, tensor by tensor.
 __global__ void __launch_bounds__(kThreads, kStepCtas8) adamw_step8_kernel(void* plan, const StepArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];
     StepShared sh;
     if (!begin_step(a, sh)) return;
     const PlanView pv = view(plan, a.n);
-    const uint32_t tid = threadIdx.x;
     const uint32_t base = smem_u32(smem);
     const int64_t c0 = a.chunks * blockIdx.x / gridDim.x, c1 = a.chunks * (blockIdx.x + 1) / gridDim.x;
     for (int64_t chunk = c0; chunk < c1;) {
         const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
-        const int64_t chunks_here = (sl.n + kChunk - 1) / kChunk;
-        const int64_t last = sl.chunk0 + chunks_here < c1 ? sl.chunk0 + chunks_here : c1;
-        const int64_t e0 = (chunk - sl.chunk0) * kChunk;                                   // elements [e0, e1)
+        const int64_t end = sl.chunk0 + (sl.n + kChunk - 1) / kChunk;
+        const int64_t last = end < c1 ? end : c1;
+        const int64_t e0 = (chunk - sl.chunk0) * kChunk;
         const int64_t e1 = sl.n < (last - sl.chunk0) * kChunk ? sl.n : (last - sl.chunk0) * kChunk;
         chunk = last;
         Rate k;
@@ -649,45 +700,17 @@ __global__ void __launch_bounds__(kThreads, kStepCtas8) adamw_step8_kernel(void*
         k.neg_lr_t = -lr * sh.inv_bc1;
         k.inv_v = sh.inv_v;
         k.eps = a.eps;
-        const int64_t full = (e1 - e0) / kGroup;
-        int64_t at = e0 + tid * kPer;
-        for (int i = 0; i < 2; ++i) {
-            if (i < full) stage_in(sl, at + i * kGroup, base + i * kStageBytes, tid);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+        const bool gf = (sl.flags & kGradF32) != 0;
+        if (sl.flags & kParamF32) {
+            if (gf) run8<kF32, true>(sl, e0, e1, a, sh, k, base);
+            else run8<kF32, false>(sl, e0, e1, a, sh, k, base);
+        } else if (a.stochastic) {
+            if (gf) run8<kBf16Stochastic, true>(sl, e0, e1, a, sh, k, base);
+            else run8<kBf16Stochastic, false>(sl, e0, e1, a, sh, k, base);
+        } else {
+            if (gf) run8<kBf16Nearest, true>(sl, e0, e1, a, sh, k, base);
+            else run8<kBf16Nearest, false>(sl, e0, e1, a, sh, k, base);
         }
-        uint32_t sm = 0, sr = 0;
-        if (full > 0) {
-            sm = sl.sm[at / 32];
-            sr = sl.sr[at / 32];
-        }
-        uint32_t cur = 0;
-        for (int64_t i = 0; i < full; ++i, at += kGroup) {
-            Raw8 x;
-            x.sm = sm;
-            x.sr = sr;
-            load_any(sl.p, (sl.flags & kParamF32) != 0, at, kPer, (sl.flags & kWide) != 0, x.p);
-            if (i + 1 < full) {
-                sm = sl.sm[(at + kGroup) / 32];
-                sr = sl.sr[(at + kGroup) / 32];
-            }
-            // the stage filled now was read one group ago
-            const uint32_t into = cur == 0 ? 2 : cur - 1;
-            if (i + 2 < full) stage_in(sl, at + 2 * kGroup, base + into * kStageBytes, tid);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-            stage_out(sl, base + cur * kStageBytes, tid, x);
-            cur = cur == 2 ? 0 : cur + 1;
-            const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
-            step8(sl, at, kPer, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
-        }
-        if (e0 + full * kGroup < e1) {   // the tensor's end
-            Raw8 x;
-            const int valid = valid_of(sl.n, at);
-            load8(sl, at, valid, x);
-            const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at);
-            step8(sl, at, valid, x, a, sh.gs, k, static_cast<uint32_t>(pos), mix(sh.key0 + static_cast<uint32_t>(pos >> 32)));
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     end_step(pv, a, sh);
 }
