@@ -83,8 +83,9 @@ __host__ __device__ inline PlanView view(void* plan, int n) {
 }
 
 // ------------------------------------------------------------------ random bits
-// Multiply, shift, multiply, shift: a bijection of 32-bit words whose output bits all depend on
-// every input bit above half way; the constants are odd and otherwise free.
+// Multiply, shift, multiply, shift: a bijection of 32-bit words.  A product carries low bits upwards,
+// a shift high bits down; after two of each, neighbouring positions differ in all 16-bit halves.  The
+// constants are odd and otherwise free.
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
     x *= 0x9E3779B1u;
     x ^= x >> 15;
@@ -403,7 +404,17 @@ __device__ __forceinline__ void nearest_params(const float (&p)[kPer], uint32_t 
 // p (1 - lr wd) - lr_t m / (r inv_v + eps), p rounded once; the denominator is normal (eps >= 1e-30)
 struct Rate {
     float keep, neg_lr_t, inv_v, eps;
+    bool finite;   // a device learning rate may be anything
 };
+__device__ __forceinline__ Rate rate_of(float lr, float wd, float inv_bc1, float inv_v, float eps) {
+    Rate k;
+    k.keep = 1.0f - lr * wd;
+    k.neg_lr_t = -lr * inv_bc1;
+    k.inv_v = inv_v;
+    k.eps = eps;
+    k.finite = isfinite(k.keep) && isfinite(k.neg_lr_t);
+    return k;
+}
 __device__ __forceinline__ float updated(float p, float m, float r, const Rate& k) {
     return fmaf(p, k.keep, k.neg_lr_t * m * rcp_approx_ftz(fmaf(r, k.inv_v, k.eps)));
 }
@@ -440,9 +451,10 @@ __device__ __forceinline__ void load8(const Slot& sl, int64_t at, int valid, Raw
 //   m = (b1 s_m) q + (c1 gs) g,   v = (root(b2) s_r q)^2 + (root(c2) gs g)^2
 // in packed pairs.  The short forms serve a warp whose blocks hold no zero, subnormal, NaN or Inf
 // and no m below E4M3's normal range under its scale -- all but a few of the warps of a weight's
-// gradient; any other warp takes the long ones.  Bound by instructions: 119 a thread's element
-// with IEEE square root and quotient and branches per element, 83 without them, about 50 with
-// packed arithmetic and the short codes.
+// gradient; any other warp takes the long ones.  Bound by instructions: 119 an element with IEEE
+// square root and quotient and branches per element, 83 without them, 67 with packed arithmetic and
+// the short codes, 61 with the loop compiled for the kind of tensor; 117 M elements (bf16 parameters,
+// fp32 gradients) in 268 us, 5.3 TB/s of its 12 bytes an element.
 template <int P>
 __device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw8& x, const StepArgs& a, float gs,
                                       const Rate& k, uint32_t pos_lo, uint32_t key) {
@@ -471,7 +483,7 @@ __device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw
     uint32_t br = block_byte(block_max(__float_as_uint(max8(r))), 0, 0x780000u);
     const float im = inv_block(bm), ir = inv_block(br);
     const uint64_t ps = add2(add2(pk2(x.p[0], x.p[1]), pk2(x.p[2], x.p[3])), add2(pk2(x.p[4], x.p[5]), pk2(x.p[6], x.p[7])));
-    const bool plain = bm != 0xFFu && br != 0xFFu && min8(m) * im >= kSmallestNormal && min8(r) * ir >= kSmallestRoot &&
+    const bool plain = k.finite && bm != 0xFFu && br != 0xFFu && min8(m) * im >= kSmallestNormal && min8(r) * ir >= kSmallestRoot &&
                        fabsf(lo2(ps) + hi2(ps)) < __uint_as_float(0x7F800000u);
     if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
@@ -509,7 +521,8 @@ __device__ __forceinline__ void step8(const Slot& sl, int64_t at, int valid, Raw
     if (p_f32 && sl.copy != nullptr) store_words(static_cast<uint16_t*>(sl.copy) + at, valid, wp);
 }
 
-// The step on 8 elements with fp32 moments.  Bound by HBM: 24 to 30 bytes an element.
+// The step on 8 elements with fp32 moments.  Bound by HBM: 24 to 30 bytes an element, 403 M elements
+// at 24 bytes in 1.44 ms (6.7 TB/s).
 __device__ __forceinline__ void step32(const Slot& sl, int64_t at, int valid, const StepArgs& a, float gs, const Rate& k,
                                        uint32_t pos_lo, uint32_t key) {
     const bool p_f32 = (sl.flags & kParamF32) != 0, wide = (sl.flags & kWide) != 0;
@@ -694,12 +707,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas8) adamw_step8_kernel(void*
         const int64_t e0 = (chunk - sl.chunk0) * kChunk;
         const int64_t e1 = sl.n < (last - sl.chunk0) * kChunk ? sl.n : (last - sl.chunk0) * kChunk;
         chunk = last;
-        Rate k;
-        const float lr = sh.lr * sl.lr_mult;
-        k.keep = 1.0f - lr * sl.wd;
-        k.neg_lr_t = -lr * sh.inv_bc1;
-        k.inv_v = sh.inv_v;
-        k.eps = a.eps;
+        const Rate k = rate_of(sh.lr * sl.lr_mult, sl.wd, sh.inv_bc1, sh.inv_v, a.eps);
         const bool gf = (sl.flags & kGradF32) != 0;
         if (sl.flags & kParamF32) {
             if (gf) run8<kF32, true>(sl, e0, e1, a, sh, k, base);
@@ -724,12 +732,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas32) adamw_step32_kernel(voi
     for (int64_t chunk = c0; chunk < c1; ++chunk) {
         const Slot sl = load_slot(pv.slots + __ldg(pv.of_chunk + chunk));
         const int64_t at = (chunk - sl.chunk0) * kChunk + threadIdx.x * kPer;
-        Rate k;
-        const float lr = sh.lr * sl.lr_mult;
-        k.keep = 1.0f - lr * sl.wd;
-        k.neg_lr_t = -lr * sh.inv_bc1;
-        k.inv_v = sh.inv_v;
-        k.eps = a.eps;
+        const Rate k = rate_of(sh.lr * sl.lr_mult, sl.wd, sh.inv_bc1, sh.inv_v, a.eps);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint64_t pos = static_cast<uint64_t>(sl.pos0 + at + h * kGroup);
@@ -741,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, kStepCtas32) adamw_step32_kernel(voi
 }
 
 // ------------------------------------------------------------------ the gradient norm
+// Bound by HBM: 403 M fp32 gradients in 224 us (7.2 TB/s); with the next runs prefetched into L2 289 us.
 // Squares are summed in fp32 over 32 elements of a thread and in 64 bits above that, in
 // a fixed order: per thread over its chunks, per warp and CTA by a tree, over the CTAs in order.
 __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) adamw_norm_kernel(void* plan, int n, int64_t chunks, float max_norm,

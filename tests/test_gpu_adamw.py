@@ -376,3 +376,15 @@ def test_binding_refuses(dev):
     with pytest.raises(mx.MxError):
         mx.adamw_state_values(plan, z(64, dtype=BF, device=dev), z(64, dtype=BF, device=dev))
     assert int(step) == 0 and not p.any()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_learning_rate_that_is_not_finite_shows(dev, bits):
+    """NaN on the device as learning rate makes bf16 parameters NaN, whichever way they are rounded: never
+    a value whose bits a rounding carry has changed."""
+    for stochastic in (False, True):
+        p = torch.full((4096,), 0.5, dtype=BF, device=dev)
+        g = torch.full((4096,), 0.25, device=dev)
+        plan, p, m, v, sm, sr, step = _one(dev, 4096, bits, g, p=p)
+        mx.adamw_step(plan, step, lr=0.0, lr_dev=torch.tensor([float("nan")], device=dev), stochastic=stochastic)
+        assert bool(torch.isnan(p).all())
