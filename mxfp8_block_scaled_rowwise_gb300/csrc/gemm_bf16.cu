@@ -8,7 +8,10 @@
 //            a(m, k)              b(n, k)                  k runs over
 //   forward  A[r0 + m][k]    k    W[e][n][k]          k    the row width
 //   dgrad    dY[r0 + m][k]   k    W[e][k][n]          n    the forward's output width
-//   wgrad    dY[r0 + k][m]   m    X[r0 + k][n]        n    the expert's rows
+//   wgrad    X[r0 + k][m]    m    dY[r0 + k][n]       n    the expert's rows
+// (wgrad computes dW[e] transposed: a thread owns an accumulator row, which is a column of dW[e],
+// so a warp's 32 threads store whole 128-byte lines.  With rows of dW[e] per thread, in 32-byte
+// pieces, 32 experts of 7168 x 2048 with 16 rows each took 409 us; this way 283.)
 // No operand is transposed in memory: tcgen05.mma takes either orientation from shared memory
 // (K contiguous, or M / N contiguous), in both cases as 128-byte rows with the 128-byte swizzle.
 //
@@ -78,10 +81,11 @@ struct Args {
     const int32_t* off;
     int E;
     int64_t R;             // rows of A (dY): off[E] may not pass it
-    int64_t m_out, n_out;  // wgrad: rows of dW[e]; all: columns of the output
+    int64_t n_out;         // columns of the output; wgrad: rows of dW[e]
+    int64_t m_out;         // wgrad: columns of dW[e]
     int64_t k_len;         // forward, dgrad: contraction length
     void* out;
-    int wide_store;        // output rows start on 32-byte boundaries: whole-sector stores
+    int wide_store;        // forward, dgrad: output rows start on 32-byte boundaries, whole-sector stores
     int* dev_err;
 };
 
@@ -89,7 +93,7 @@ struct Tile {
     int e;
     int64_t row0;          // first row of the expert
     int64_t m_in;          // this CTA's first tile row: within the expert's rows, or within m_out
-    int64_t n0;            // first output column of the tile
+    int64_t n0;            // first output column of the tile (wgrad: row of dW[e])
     int num_kt;            // K steps
     int tail;              // wgrad: rows of the last K step that are the expert's, 0 if all 64
     int last_k16;          // wgrad: MMAs (16 rows deep) that the last K step takes
@@ -498,18 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 if (row_ok) {
-                    float* dst = static_cast<float*>(g.out) + (t.e * g.m_out + t.m_in + row) * g.n_out + col0;
+                    const int64_t left = g.n_out - col0;
+                    const int cols = static_cast<int>(left < 128 ? left : 128);
+                    float* dst = static_cast<float*>(g.out) + (t.e * g.n_out + col0) * g.m_out + t.m_in + row;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (col0 + 8 * j < g.n_out) {
-                            const uint32_t* s = sum[j / 4] + 8 * (j % 4);
-                            if (g.wide_store) {
-                                st_global_v8(dst + 8 * j, s[0], s[1], s[2], s[3], s[4], s[5], s[6], s[7], l2_policy_evict_first());
-                            } else {
-                                reinterpret_cast<uint4*>(dst)[2 * j] = make_uint4(s[0], s[1], s[2], s[3]);
-                                reinterpret_cast<uint4*>(dst)[2 * j + 1] = make_uint4(s[4], s[5], s[6], s[7]);
-                            }
-                        }
+                    for (int j = 0; j < 128; ++j) {
+                        if (j < cols) __stcs(reinterpret_cast<uint32_t*>(dst), sum[j / 32][j % 32]);
+                        dst += g.m_out;
                     }
                 }
             } else {
@@ -847,7 +846,7 @@ int launch_tiles(const Problem& pr, const Args& g, int dev, int num_sms, cudaStr
     }
     CUtensorMap tmA, tmB;
     const bool ok =
-        kW ? make_map(&tmA, pr.A, 1, g.R, pr.N, BK, false) && make_map(&tmB, pr.B, 1, g.R, pr.K, BK, false)
+        kW ? make_map(&tmA, pr.B, 1, g.R, pr.K, BK, false) && make_map(&tmB, pr.A, 1, g.R, pr.N, BK, false)
         : PASS == kBf16Fwd
             ? make_map(&tmA, pr.A, 1, g.R, pr.K, BM, false) && make_map(&tmB, pr.B, g.E, pr.N, pr.K, C::kBRows, true)
             : make_map(&tmA, pr.A, 1, g.R, pr.K, BM, false) && make_map(&tmB, pr.B, g.E, pr.K, pr.N, BK, true);
@@ -896,11 +895,11 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
     g.off = off;
     g.E = E;
     g.R = R;
-    g.m_out = w ? N : 0;
-    g.n_out = w ? K : N;
+    g.m_out = w ? K : 0;
+    g.n_out = N;
     g.k_len = w ? 0 : K;
     g.out = out;
-    g.wide_store = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && (w || N % 16 == 0) ? 1 : 0;
+    g.wide_store = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && N % 16 == 0 ? 1 : 0;
     g.dev_err = dev_err;
     const Problem pr{A, B, N, K};
     const int n = num_sms[dev];
@@ -920,7 +919,7 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
     // pairs (us), 32 experts of 4096 x 7168: forward at 128 rows per expert 310 / 326, 256 rows 467 /
     // 440, 1024 rows 1286 / 1224; 128 experts of very uneven popularity, 256 rows on average 372 / 400.
     // Weight gradient of 7168 x 2048 at 16 rows 418 / 443, 128 rows 440 / 448; of 128 columns 20 / 29.
-    const bool pairs = w ? N > BM && R > 128 * static_cast<int64_t>(E) : R >= 512 * static_cast<int64_t>(E);
+    const bool pairs = w ? K > BM && R > 128 * static_cast<int64_t>(E) : R >= 512 * static_cast<int64_t>(E);
     if (pass == kBf16Fwd)
         return pairs ? launch_tiles<2, kBf16Fwd>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Fwd>(pr, g, dev, n, stream);
     if (pass == kBf16Dgrad)
