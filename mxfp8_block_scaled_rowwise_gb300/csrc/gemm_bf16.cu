@@ -69,8 +69,13 @@ struct Cfg {
     static constexpr uint32_t kBBytes = kBRows * kRowBytes;
     static constexpr uint32_t kOffA = 0;
     static constexpr uint32_t kOffB = kSlots * kABytes;
-    static constexpr uint32_t kOffBar = kOffB + kSlots * kBBytes;
-    static constexpr uint32_t kNumBars = 3 * kStages + 5;         // full[], empty[], tail[], tmem_full[2], tmem_empty[2], drain
+    static constexpr uint32_t kTailA = BM * 2 * 16;               // wgrad: an expert's last rows of a, 16 deep,
+    static constexpr uint32_t kTailB = kBRows * 2 * 16;           // and of b
+    static constexpr uint32_t kTailBytes = kTailA + kTailB;
+    static constexpr uint32_t kOffTail = kOffB + kSlots * kBBytes;
+    static constexpr uint32_t kOffBar = kOffTail + 2 * kTailBytes;
+    // full[], empty[], tmem_full[2], tmem_empty[2], tail_full[2], tail_empty[2], drain
+    static constexpr uint32_t kNumBars = 2 * kStages + 9;
     static constexpr uint32_t kOffMisc = kOffBar + kNumBars * 8;  // tmem base, abort flag
     static constexpr uint32_t kOffTable = (kOffMisc + 8 + 15) / 16 * 16;
     static constexpr uint32_t kSmemBytes = kOffTable + (kMaxE + 1) * 4 + 1024;
@@ -84,6 +89,8 @@ struct Args {
     int64_t n_out;         // columns of the output; wgrad: rows of dW[e]
     int64_t m_out;         // wgrad: columns of dW[e]
     int64_t k_len;         // forward, dgrad: contraction length
+    const void* a;         // wgrad: the operands (the copies take them from the tensor maps)
+    const void* b;
     void* out;
     int wide_store;        // forward, dgrad: output rows start on 32-byte boundaries, whole-sector stores
     int* dev_err;
@@ -94,9 +101,9 @@ struct Tile {
     int64_t row0;          // first row of the expert
     int64_t m_in;          // this CTA's first tile row: within the expert's rows, or within m_out
     int64_t n0;            // first output column of the tile (wgrad: row of dW[e])
-    int num_kt;            // K steps
-    int tail;              // wgrad: rows of the last K step that are the expert's, 0 if all 64
+    int num_kt;            // K steps; wgrad: that hold 16 rows of the expert or more
     int last_k16;          // wgrad: MMAs (16 rows deep) that the last K step takes
+    int tail;              // wgrad: rows after the last multiple of 16
     int valid_rows;        // of this CTA's 128
 };
 
@@ -140,9 +147,10 @@ __device__ __forceinline__ Tile get_tile(const Args& g, const int32_t* table, ui
     const uint32_t ntile = local / gs;
     t.m_in = static_cast<int64_t>(grp * G + (local - ntile * gs)) * TM + rank * BM;
     t.n0 = static_cast<int64_t>(ntile) * BN;
-    t.num_kt = static_cast<int>((k + BK - 1) / BK);
-    t.tail = WGRAD ? static_cast<int>(k % BK) : 0;
-    t.last_k16 = t.tail == 0 ? BK / 16 : (t.tail + 15) / 16;
+    const uint32_t whole = WGRAD ? k & ~15u : k;
+    t.num_kt = static_cast<int>((whole + BK - 1) / BK);
+    t.last_k16 = static_cast<int>((whole + BK - 1) % BK / 16) + 1;
+    t.tail = WGRAD ? static_cast<int>(k % 16) : 0;
     const int64_t vr = static_cast<int64_t>(rows) - t.m_in;
     t.valid_rows = static_cast<int>(vr < 0 ? 0 : (vr < BM ? vr : BM));
     return t;
@@ -182,25 +190,25 @@ __device__ __forceinline__ bool build_table(const Args& g, int32_t* table, int l
 }
 
 // Loads of one K step: this CTA's 128 rows of a and kBRows of b (from row b0 = its first b row).
-// G selects whether the copies complete on a barrier in the pair's leader (2) or in this CTA (1).
-template <int NC, int PASS, int G>
+// A pair's copies complete on a barrier in its leader.
+template <int NC, int PASS>
 __device__ __forceinline__ void load_step(const CUtensorMap* tmA, const CUtensorMap* tmB, uint32_t sa, uint32_t sb,
                                           uint32_t bar, const Tile& t, int kt, int32_t b0) {
     const int32_t k0 = kt * BK;
     const int32_t row0 = static_cast<int32_t>(t.row0), m = static_cast<int32_t>(t.m_in);
     if constexpr (PASS != kBf16Wgrad) {
-        tma_load_2d_g<G>(sa, tmA, bar, k0, row0 + m);
+        tma_load_2d_g<NC>(sa, tmA, bar, k0, row0 + m);
     } else {
 #pragma unroll
-        for (int i = 0; i < BM / 64; ++i) tma_load_2d_g<G>(sa + i * 64 * kRowBytes, tmA, bar, m + 64 * i, row0 + k0);
+        for (int i = 0; i < BM / 64; ++i) tma_load_2d_g<NC>(sa + i * 64 * kRowBytes, tmA, bar, m + 64 * i, row0 + k0);
     }
     if constexpr (PASS == kBf16Fwd) {
-        tma_load_3d_g<G>(sb, tmB, bar, k0, b0, t.e);
+        tma_load_3d_g<NC>(sb, tmB, bar, k0, b0, t.e);
     } else {
 #pragma unroll
         for (int i = 0; i < Cfg<NC>::kBRows / 64; ++i) {
-            if constexpr (PASS == kBf16Dgrad) tma_load_3d_g<G>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, k0, t.e);
-            else tma_load_2d_g<G>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, row0 + k0);
+            if constexpr (PASS == kBf16Dgrad) tma_load_3d_g<NC>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, k0, t.e);
+            else tma_load_2d_g<NC>(sb + i * 64 * kRowBytes, tmB, bar, b0 + 64 * i, row0 + k0);
         }
     }
 }
@@ -215,10 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar_full = sbase + C::kOffBar;                     // + 8 * stage (used in the leader)
     const uint32_t bar_empty = bar_full + 8 * C::kStages;             // + 8 * stage
-    const uint32_t bar_tail = bar_full + 16 * C::kStages;             // + 8 * stage: this CTA's copies of a ragged last stage
-    const uint32_t bar_tmem_full = bar_full + 24 * C::kStages;        // + 8 * accumulator
+    const uint32_t bar_tmem_full = bar_full + 16 * C::kStages;        // + 8 * accumulator
     const uint32_t bar_tmem_empty = bar_tmem_full + 16;               // + 8 * accumulator (used in the leader)
-    const uint32_t bar_drain = bar_tmem_full + 32;
+    const uint32_t bar_tail_full = bar_tmem_full + 32;                // + 8 * buffer (used in the leader)
+    const uint32_t bar_tail_empty = bar_tmem_full + 48;               // + 8 * buffer
+    const uint32_t bar_drain = bar_tmem_full + 64;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     int32_t* table = reinterpret_cast<int32_t*>(smem + C::kOffTable);
@@ -230,19 +239,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t unit = blockIdx.x / NC;
     const int64_t num_units = gridDim.x / NC;
     const uint32_t lead_full = NC == 2 ? mapa_shared(bar_full, 0) : bar_full;
+    const uint32_t lead_tail_full = NC == 2 ? mapa_shared(bar_tail_full, 0) : bar_tail_full;
     const uint32_t lead_tmem_empty = NC == 2 ? mapa_shared(bar_tmem_empty, 0) : bar_tmem_empty;
     const uint16_t pair_ctas = static_cast<uint16_t>(NC == 2 ? 0x3 : 0x1);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            // wgrad: one arrival per CTA (its producer, or for a ragged last stage its zeroing warp)
-            mbar_init(bar_full + 8 * s, kW ? NC : 1);
+            mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
-            mbar_init(bar_tail + 8 * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(bar_tmem_full + 8 * a, 1);
             mbar_init(bar_tmem_empty + 8 * a, kNumEpiWarps * NC);
+            mbar_init(bar_tail_full + 8 * a, 2 * NC);
+            mbar_init(bar_tail_empty + 8 * a, 1);
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -276,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             int64_t issued = 0;
-            uint32_t tails = 0;   // bit s: parity of the next tail phase of stage s; bit 8 + s: one was issued
             bool ok = true;
             for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
                 const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
@@ -288,24 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const uint32_t bytes = static_cast<uint32_t>(nsub) * (C::kABytes + C::kBBytes);
-                    if (kW && t.tail % 16 != 0 && kt + nsub == t.num_kt) {
-                        // the ragged last stage: to this CTA's own barrier, for the zeroing warp
-                        mbar_arrive_expect_tx(bar_tail + 8 * stage, bytes);
-                        for (int sub = 0; sub < nsub; ++sub) {
-                            const int slot = stage * C::kSub + sub;
-                            load_step<NC, PASS, 1>(&tmA, &tmB, sbase + C::kOffA + slot * C::kABytes,
-                                                   sbase + C::kOffB + slot * C::kBBytes, bar_tail + 8 * stage, t, kt + sub, b0);
-                        }
-                        tails = (tails ^ (1u << stage)) | (0x100u << stage);
-                    } else {
-                        if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, NC * bytes);
-                        else if (kW) mbar_arrive_cluster_relaxed(lead_full + 8 * stage);
-                        for (int sub = 0; sub < nsub; ++sub) {
-                            const int slot = stage * C::kSub + sub;
-                            load_step<NC, PASS, NC>(&tmA, &tmB, sbase + C::kOffA + slot * C::kABytes,
-                                                    sbase + C::kOffB + slot * C::kBBytes, lead_full + 8 * stage, t,
-                                                    kt + sub, b0);
-                        }
+                    if (leader) mbar_arrive_expect_tx(bar_full + 8 * stage, NC * bytes);
+                    for (int sub = 0; sub < nsub; ++sub) {
+                        const int slot = stage * C::kSub + sub;
+                        load_step<NC, PASS>(&tmA, &tmB, sbase + C::kOffA + slot * C::kABytes,
+                                            sbase + C::kOffB + slot * C::kBBytes, lead_full + 8 * stage, t, kt + sub, b0);
                     }
                     ++issued;
                     if (++stage == C::kStages) {
@@ -319,8 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 atomicOr(g.dev_err, MX_DEVERR_TIMEOUT);
             }
             // let the copies still in flight land before exit
-            for (int s = 0; s < C::kStages; ++s)
-                if ((tails >> (8 + s)) & 1u) mbar_wait_timeout(bar_tail + 8 * s, ((tails >> s) & 1u) ^ 1u, kWaitLimitNs / 4);
             if (leader) {
                 const int64_t outstanding = issued < C::kStages ? issued : C::kStages;
                 for (int64_t i = 1; i <= outstanding; ++i) {
@@ -343,27 +337,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 1 KiB apart; 16 K = two groups further.
             constexpr uint32_t kLboA = kW ? 64 * kRowBytes : 16, kLboB = PASS != kBf16Fwd ? 64 * kRowBytes : 16;
             constexpr uint64_t kStepA = kW ? 2048 >> 4 : 32 >> 4, kStepB = PASS != kBf16Fwd ? 2048 >> 4 : 32 >> 4;
+            uint32_t tails = 0;      // chunks of last rows multiplied: buffer tails & 1
+            auto begin = [&]() {
+                if (!mbar_wait_bounded(bar_tmem_empty + 8 * (acc_iter & 1u), ((acc_iter >> 1) & 1u) ^ 1u, abort_flag,
+                                       kWaitLimitNs))
+                    return false;
+                tc_fence_after();
+                return true;
+            };
+            auto multiply_tail = [&](bool first) {
+                const uint32_t buf = tails & 1u, parity = (tails >> 1) & 1u;
+                if (!(NC == 2 ? mbar_wait_bounded_cluster(bar_tail_full + 8 * buf, parity, abort_flag, kWaitLimitNs)
+                              : mbar_wait_bounded(bar_tail_full + 8 * buf, parity, abort_flag, kWaitLimitNs)))
+                    return false;
+                tc_fence_after();
+                const uint32_t sa = sbase + C::kOffTail + buf * C::kTailBytes;
+                mma_bf16_g<NC>(tmem_base + (acc_iter & 1u) * BN, smem_desc(sa, 16 * kRowBytes, 1024, 2),
+                               smem_desc(sa + C::kTailA, 16 * kRowBytes, 1024, 2), idesc, first ? 0u : 1u);
+                tc_commit_g<NC>(bar_tail_empty + 8 * buf, pair_ctas);
+                ++tails;
+                return true;
+            };
             for (int64_t L = unit; L < total_tiles && ok; L += num_units) {
                 const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
-                for (int kt = 0; kt < t.num_kt && ok; kt += C::kSub) {
-                    const uint32_t acc = acc_iter & 1u;
+                for (int kt = 0; kt < t.num_kt; kt += C::kSub) {
                     const bool first = kW ? kt % kPartSteps == 0 : kt == 0;
-                    if (first) {
-                        if (!mbar_wait_bounded(bar_tmem_empty + 8 * acc, ((acc_iter >> 1) & 1u) ^ 1u, abort_flag,
-                                               kWaitLimitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
+                    if (first && !(ok = begin())) break;
                     const int nsub = t.num_kt - kt < C::kSub ? t.num_kt - kt : C::kSub;
-                    const bool there = kW && NC == 2
-                                           ? mbar_wait_bounded_cluster(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs)
-                                           : mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs);
-                    if (!there) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(ok = mbar_wait_bounded(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int sub = 0; sub < C::kSub; ++sub) {
@@ -375,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < BK / 16; ++k)
                                 if (!kW || k < k16)
-                                    mma_bf16_g<NC>(tmem_base + acc * BN, adesc + k * kStepA, bdesc + k * kStepB, idesc,
-                                                   (first && sub == 0 && k == 0) ? 0u : 1u);
+                                    mma_bf16_g<NC>(tmem_base + (acc_iter & 1u) * BN, adesc + k * kStepA, bdesc + k * kStepB,
+                                                   idesc, (first && sub == 0 && k == 0) ? 0u : 1u);
                         }
                     }
                     tc_commit_g<NC>(bar_empty + 8 * stage, pair_ctas);
@@ -386,9 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int next = kt + C::kSub;
                     if (next >= t.num_kt || (kW && next % kPartSteps == 0)) {
-                        tc_commit_g<NC>(bar_tmem_full + 8 * acc, pair_ctas);
+                        if (kW && next >= t.num_kt && t.tail != 0 && !(ok = multiply_tail(false))) break;
+                        tc_commit_g<NC>(bar_tmem_full + 8 * (acc_iter & 1u), pair_ctas);
                         ++acc_iter;
                     }
+                }
+                if (kW && ok && t.num_kt == 0 && t.tail != 0) {
+                    if (!(ok = begin() && multiply_tail(true))) break;
+                    tc_commit_g<NC>(bar_tmem_full + 8 * (acc_iter & 1u), pair_ctas);
+                    ++acc_iter;
                 }
             }
             if (!ok) {
@@ -399,18 +406,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit_g<NC>(bar_drain, static_cast<uint16_t>(0x1));
             mbar_wait_timeout(bar_drain, 0, kWaitLimitNs / 4);
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ wgrad: ragged last stages
-        if (kW) {
-            int64_t stages = 0;
-            uint32_t tails = 0;   // bit s: parity of stage s's next tail phase
+    } else if (warp < kEpiWarp0) {
+        // ------------------------------------------------------------ wgrad: an expert's last rows
+        if constexpr (kW) {
+            constexpr int kPieces = C::kTailBytes / 16 / 64;   // 16-byte pieces per thread of the two warps
+            const uint4* a = static_cast<const uint4*>(g.a);
+            const uint4* b = static_cast<const uint4*>(g.b);
+            uint32_t tails = 0;
             for (int64_t L = unit; L < total_tiles; L += num_units) {
                 const Tile t = get_tile<NC, kW>(g, table, static_cast<uint32_t>(L), rank);
-                stages += (t.num_kt + C::kSub - 1) / C::kSub;
-                if (t.tail % 16 == 0) continue;
-                const int stage = static_cast<int>((stages - 1) % C::kStages);
+                if (t.tail == 0) continue;
+                const int64_t row0 = t.row0 + (t.num_kt == 0 ? 0 : (t.num_kt - 1) * BK + t.last_k16 * 16);
+                uint4 v[kPieces];
+                // piece: 8 of 64 columns (a's boxes of 64, then b's), of one of 16 rows
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int p = i * 64 + (warp - 2) * 32 + lane;
+                    const int box = p / 128, row = p / 8 % 16, piece = p % 8;
+                    const bool is_a = box < BM / 64;
+                    const int64_t col = is_a ? t.m_in + box * 64 + piece * 8
+                                             : t.n0 + rank * C::kBRows + (box - BM / 64) * 64 + piece * 8;
+                    const int64_t width = is_a ? g.m_out : g.n_out;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < t.tail && col < width) v[i] = __ldg((is_a ? a : b) + ((row0 + row) * width + col) / 8);
+                }
+                const uint32_t buf = tails & 1u;
                 uint32_t okw = 1;
-                if (lane == 0) okw = mbar_wait_bounded(bar_tail + 8 * stage, (tails >> stage) & 1u, abort_flag, kWaitLimitNs) ? 1u : 0u;
+                if (lane == 0)
+                    okw = mbar_wait_bounded(bar_tail_empty + 8 * buf, ((tails >> 1) & 1u) ^ 1u, abort_flag, kWaitLimitNs) ? 1u : 0u;
                 okw = __shfl_sync(0xffffffffu, okw, 0);
                 if (!okw) {
                     if (lane == 0) {
@@ -420,24 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 __syncwarp();
-                tails ^= 1u << stage;
-                const int slot = stage * C::kSub + (t.num_kt - 1) % C::kSub;
-                // 128-byte rows from tail up to the last MMA's depth in every 64-row box (the swizzle stays
-                // inside a row); no MMA reads the rows after those
-                uint8_t* a = smem + C::kOffA + slot * C::kABytes;
-                uint8_t* b = smem + C::kOffB + slot * C::kBBytes;
-                const int pieces = (16 - t.tail % 16) * 8;   // 16-byte pieces per box
-                for (int i = 0; i < BM / 64 + C::kBRows / 64; ++i) {
-                    uint8_t* box = i < BM / 64 ? a + i * 64 * kRowBytes : b + (i - BM / 64) * 64 * kRowBytes;
-                    uint4* p = reinterpret_cast<uint4*>(box + t.tail * kRowBytes);
-                    for (int j = lane; j < pieces; j += 32) p[j] = make_uint4(0u, 0u, 0u, 0u);
+                uint8_t* dst = smem + C::kOffTail + buf * C::kTailBytes;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int p = i * 64 + (warp - 2) * 32 + lane;
+                    const int box = p / 128, row = p / 8 % 16, piece = p % 8;
+                    *reinterpret_cast<uint4*>(dst + (box * 16 + row) * kRowBytes + ((piece ^ (row & 7)) * 16)) = v[i];
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
-                    if (NC == 2) mbar_arrive_cluster_release(lead_full + 8 * stage);
-                    else mbar_arrive(bar_full + 8 * stage);
+                    if (NC == 2) mbar_arrive_cluster_release(lead_tail_full + 8 * buf);
+                    else mbar_arrive(bar_tail_full + 8 * buf);
                 }
+                ++tails;
             }
         }
     } else if (warp >= kEpiWarp0) {
@@ -475,15 +494,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
             if constexpr (kW) {
                 uint32_t sum[4][32];   // fp32 bits: the first part is loaded as it is, later ones added
-                if (t.num_kt == 0) {   // an expert without rows
+                const int parts = t.num_kt == 0 ? t.tail != 0 : (t.num_kt + kPartSteps - 1) / kPartSteps;
+                if (parts == 0) {   // an expert without rows
 #pragma unroll
                     for (int j = 0; j < 128; ++j) sum[j / 32][j % 32] = 0u;
                 }
                 bool ok = true;
-                for (int kt = 0; kt < t.num_kt; kt += kPartSteps) {
+                for (int part = 0; part < parts; ++part) {
                     if (!(ok = acquire())) break;
                     const uint32_t taddr = tmem_base + lanes + (acc_iter & 1u) * BN + half * 128;
-                    if (kt == 0) {
+                    if (part == 0) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(taddr + c * 32, sum[c]);
                         tmem_ld_wait();
@@ -898,6 +918,8 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
     g.m_out = w ? K : 0;
     g.n_out = N;
     g.k_len = w ? 0 : K;
+    g.a = B;               // used by wgrad: X
+    g.b = A;               // and dY
     g.out = out;
     g.wide_store = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 && N % 16 == 0 ? 1 : 0;
     g.dev_err = dev_err;
