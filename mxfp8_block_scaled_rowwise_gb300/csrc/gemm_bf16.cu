@@ -18,15 +18,16 @@
 // Ragged edges.  An expert's rows are dense, so a tile of A rows can reach into the next expert's
 // rows: those only feed accumulator rows that are never stored.  Widths that no tile divides end
 // in zeros that the tensor copies fill in (the weights have a dimension of their own for the
-// expert, so a tile never reads the next expert's).  Only wgrad contracts over rows: an expert's
-// last K step stops after the MMA, 16 rows deep, that takes its last row.  That MMA would add up to
-// 15 rows of the next expert, and a NaN there times a zero would not vanish, so one warp per CTA
-// overwrites those rows of both operands with zeros in shared memory before the MMA sees the stage
-// (32 groups of 512 rows on average, 7168 x 2048: 692 us, and 706 us with all 64 rows of the step
-// zeroed and multiplied; groups of 16 rows: 410 and 418 us).
+// expert, so a tile never reads the next expert's).  Only wgrad contracts over rows.  Its K steps
+// stop at the expert's last multiple of 16 rows, the depth of one MMA; what the copies bring in
+// after it is not multiplied.  The up to 15 rows that remain would share an MMA with the next
+// expert's, and a NaN there times a zero would not vanish.  So two warps load them by themselves,
+// with zeros after the last, into one of two buffers beside the pipeline, a tile ahead of the MMA.
+// (Zeroing those rows where the copies had put them, in the last stage, held every tile up by about
+// 1.6 us: 32 experts of 7168 x 2048, 512 rows each, took 657 us and take 508.)
 //
 // Roles of the 12 warps: 0 issues the tensor copies, 1 (one lane of the leader CTA) the MMAs, 2
-// builds the tile list and zeroes wgrad's ragged ends, 4 to 11 drain the accumulators.  With
+// builds the tile list, 2 and 3 fill wgrad's last rows in, 4 to 11 drain the accumulators.  With
 // NC = 2 a cluster of two CTAs computes 256 x 256 tiles with cta_group::2 MMAs, each CTA staging
 // its 128 rows of a and one half of b; with NC = 1 a CTA computes 128 x 256 tiles.  The 512
 // columns of tensor memory hold two accumulators, so a tile is drained while the next one is
@@ -940,8 +941,9 @@ int launch_grouped_gemm_bf16(int pass, const void* A, const void* B, const int32
     // CTA pairs for long groups, single CTAs (finer tiles, no cluster to start) for short ones.  Single /
     // pairs (us), 32 experts of 4096 x 7168: forward at 128 rows per expert 310 / 326, 256 rows 467 /
     // 440, 1024 rows 1286 / 1224; 128 experts of very uneven popularity, 256 rows on average 372 / 400.
-    // Weight gradient of 7168 x 2048 at 16 rows 418 / 443, 128 rows 440 / 448; of 128 columns 20 / 29.
-    const bool pairs = w ? K > BM && R > 128 * static_cast<int64_t>(E) : R >= 512 * static_cast<int64_t>(E);
+    // Weight gradient of 7168 x 2048 at 16 rows 283 / 311, 256 rows 360 / 370, 512 rows 584 / 505; of 128
+    // columns (2048 x 128) at 128 rows 12 / 20, 1024 rows 34 / 41.
+    const bool pairs = w ? K > BM && R > 256 * static_cast<int64_t>(E) : R >= 512 * static_cast<int64_t>(E);
     if (pass == kBf16Fwd)
         return pairs ? launch_tiles<2, kBf16Fwd>(pr, g, dev, n, stream) : launch_tiles<1, kBf16Fwd>(pr, g, dev, n, stream);
     if (pass == kBf16Dgrad)
