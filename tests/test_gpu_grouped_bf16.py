@@ -142,6 +142,29 @@ def test_other_experts_and_dropped_rows_stay_out(dev, counts, N, K):
         assert torch.equal(C2[s], C[s]) and torch.equal(dX2[s], dX[s]) and torch.equal(dW2[e], dW[e])
 
 
+@pytest.mark.parametrize("counts,N,K", [([1029, 271, 0, 1300, 15], 264, 392), ([512, 528, 513, 527, 16], 136, 264),
+                                        ([577, 1, 31, 1041], 520, 128)])
+def test_last_rows_of_long_groups(dev, counts, N, K):
+    """Groups long enough for pairs of CTAs, ending 0, 1, 15 and other numbers of rows after a
+    multiple of 16, right at and right after the 512 rows of a partial sum: each expert's gradient
+    against 64 bits, and unchanged bit for bit by NaN and Inf in its neighbours' rows."""
+    a, dy, w, off, R, E = _make(counts, N, K, dev, 47, extra=20)
+    err = mx.new_dev_err(dev)
+    dW, dW2 = (torch.full((E, N, K), 7.0, dtype=torch.float32, device=dev) for _ in range(2))
+    mx.grouped_gemm_bf16_wgrad(dy, a, off, E, R, N, K, dW, err)
+    check_dev_err(err)
+    _check_wgrad(dW, dy, a, counts)
+    o = offsets(counts)[0]
+    for e, c in enumerate(counts):
+        a2, dy2 = a.clone(), dy.clone()
+        for t in (a2, dy2):
+            t[:o[e]] = float("nan")
+            t[o[e + 1]:] = float("inf")
+        mx.grouped_gemm_bf16_wgrad(dy2, a2, off, E, R, N, K, dW2, err)
+        check_dev_err(err)
+        assert torch.equal(dW2[e], dW[e])
+
+
 def test_gradients_are_differences_of_the_forward(dev):
     """On small integers every sum is exact, so the change of L = sum C dY under a unit step of one
     input element is that element's gradient, exactly."""
